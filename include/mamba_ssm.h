@@ -425,6 +425,136 @@ int mamba_state_update_mimo(float *state, const void *x, const void *delta,
 /* 1 if mamba_selective_scan_mimo implements this number of inputs/outputs and states. */
 int mamba_mimo_supported(int64_t ranks, int64_t nstate);
 
+/*
+ * Gated linear recurrence: the scan's element-wise relative, with one state
+ * per channel and its decay given per token instead of by A, Delta, B and C.
+ *
+ * Defined by: the recurrence h_t = Abar h_{t-1} + Bbar x_t of section
+ * "Ayrık Zamana Geçiş" with one state per channel, whose Abar is an input
+ * (the selectivity of section "Mamba'nın Yeniliği: Selective SSM" taken to
+ * the transition itself); the pages print no such form.  For each (batch,
+ * channel), from the gate g and the input x:
+ *   a_t = 1 / (1 + exp(-g_t))          (default)
+ *   a_t = exp(g_t)                     (MAMBA_GATE_LOG; g_t <= 0)
+ *   h_t = a_t h_{t-1} + w_t x_t,   w_t = 1, or 1 - a_t (MAMBA_GATE_CONVEX)
+ *   y_t = h_t
+ * A gate of minus infinity (or the type's lowest value) is a_t = 0 in both
+ * forms: h_t = w_t x_t exactly, and nothing flows back past token t.  That
+ * starts a new sequence inside a packed one.
+ *
+ *   x, gate, y       device, dtype, [batch][len][channels]  (y: output)
+ *   initial_state    device, float32, [batch][channels], or NULL (zeros)
+ *   final_state      device, float32, [batch][channels], or NULL; receives h
+ *                    after the last token (len == 0: initial_state, or zeros)
+ *   checkpoints      device, float32, [batch][blocks][channels] with blocks =
+ *                    ceil(len / MAMBA_GATED_SCAN_BLOCK), or NULL; receives the
+ *                    state entering every block of tokens, which spares
+ *                    mamba_gated_scan_backward a pass over x and gate
+ *   flags            bitwise OR of MAMBA_GATE_*; unknown bits give
+ *                    MAMBA_ERR_INVALID_ARG
+ *
+ * Any number of channels; every pointer aligned to its element size.
+ * Not checked: x, states and (but for minus infinity) gates finite, and
+ * gates at most 0 with MAMBA_GATE_LOG.  batch * len and batch * channels
+ * must stay below 2^31 (MAMBA_ERR_UNSUPPORTED).  Stream-ordered scratch, asynchrony
+ * and errors as for mamba_selective_scan; an output that overlaps an input
+ * or another output (final_state on initial_state, say) gives
+ * MAMBA_ERR_INVALID_ARG, here and in the calls below.  Results do not change
+ * from call to call.
+ */
+#define MAMBA_GATE_LOG 1u
+#define MAMBA_GATE_CONVEX 2u
+#define MAMBA_GATED_SCAN_BLOCK 256
+
+int mamba_gated_scan(const void *x, const void *gate, const float *initial_state,
+                     void *y, float *final_state, float *checkpoints,
+                     int64_t batch, int64_t len, int64_t channels,
+                     unsigned flags, int dtype, mamba_stream_t stream);
+
+/*
+ * Gradients of mamba_gated_scan, given dy = dL/dy and d_final_state =
+ * dL/dh_final (NULL: zero), by reverse-mode differentiation:
+ *   lam_t = dy_t + a_{t+1} lam_{t+1}      (the last token's: + d_final_state)
+ *   dx_t = w_t lam_t
+ *   dg_t = lam_t (h_{t-1} - [x_t, MAMBA_GATE_CONVEX]) da/dg,
+ *          da/dg = a_t (1 - a_t), or a_t with MAMBA_GATE_LOG
+ *   d_initial_state = a_0 lam_0
+ *
+ *   x, gate, initial_state, flags   as the forward call's
+ *   checkpoints       what the forward call with the same x, gate and
+ *                     initial_state wrote there (initial_state is then not
+ *                     read), or NULL: computed again
+ *   dy                device, dtype, [batch][len][channels]
+ *   dx, dgate         device, dtype, [batch][len][channels] (outputs)
+ *   d_initial_state   device, float32, [batch][channels], or NULL (output;
+ *                     len == 0: d_final_state, or zeros)
+ * The states between the blocks are computed again in float32 (never read
+ * back from y, which is rounded).  Sizes, alignment, scratch, asynchrony and
+ * errors as for mamba_gated_scan.
+ */
+int mamba_gated_scan_backward(const void *x, const void *gate, const float *initial_state,
+                              const float *checkpoints, const void *dy, const float *d_final_state,
+                              void *dx, void *dgate, float *d_initial_state,
+                              int64_t batch, int64_t len, int64_t channels,
+                              unsigned flags, int dtype, mamba_stream_t stream);
+
+/*
+ * One token of the gated recurrence for every (batch, channel), for
+ * generation: state <- a state + w x, y = state.
+ *   state        device, float32, [batch][channels], updated in place
+ *   x, gate, y   device, dtype, [batch][channels] (y: output)
+ * flags and sizes as mamba_gated_scan.  No scratch memory is used.
+ */
+int mamba_gated_step(float *state, const void *x, const void *gate, void *y,
+                     int64_t batch, int64_t channels, unsigned flags, int dtype, mamba_stream_t stream);
+
+/*
+ * Layer norm of rows of channels, the norm around a scan in a model's block
+ * (a linear recurrence's state has no bound of its own).  For each row, n =
+ * channels:
+ *   mean = sum(x) / n                          (0 with MAMBA_NORM_RMS)
+ *   rstd = (sum((x - mean)^2) / n + eps)^(-1/2)
+ *   y = (x - mean) rstd weight + bias
+ * The variance is summed from x - mean, never as a difference of sums.
+ *
+ *   x, y           device, dtype, [rows][channels]  (y: output)
+ *   weight, bias   device, float32, [channels], or NULL (ones, zeros)
+ *   mean, rstd     device, float32, [rows], or NULL (outputs, for the backward)
+ *   eps            finite, >= 0
+ *   flags          0 or MAMBA_NORM_RMS
+ * channels at most MAMBA_NORM_MAX_CHANNELS and rows below 2^31
+ * (MAMBA_ERR_UNSUPPORTED).  Every pointer aligned to its element size.
+ * rows == 0 or channels == 0 is a no-op.  No scratch memory is used.
+ */
+#define MAMBA_NORM_RMS 1u
+#define MAMBA_NORM_MAX_CHANNELS 16384
+
+int mamba_layer_norm(const void *x, const float *weight, const float *bias, void *y,
+                     float *mean, float *rstd, int64_t rows, int64_t channels, float eps,
+                     unsigned flags, int dtype, mamba_stream_t stream);
+
+/*
+ * Gradients of mamba_layer_norm.  With xh = (x - mean) rstd, d = dy weight
+ * and averages over a row's channels:
+ *   dx = rstd (d - avg(d) - xh avg(d xh))      (MAMBA_NORM_RMS: without avg(d))
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ *
+ *   dy, x        device, dtype, [rows][channels]
+ *   mean, rstd   what the forward call wrote (mean is not read with
+ *                MAMBA_NORM_RMS and may then be NULL)
+ *   dx           device, dtype, [rows][channels] (output)
+ *   dweight, dbias   device, float32, [channels], or NULL where not wanted
+ *                (outputs; zeros when rows == 0)
+ * The sums over rows are taken in a fixed order (no atomic additions), so
+ * results do not change from call to call.  Stream-ordered scratch as for
+ * mamba_selective_scan.  Sizes and errors as for mamba_layer_norm.
+ */
+int mamba_layer_norm_backward(const void *dy, const void *x, const float *weight,
+                              const float *mean, const float *rstd,
+                              void *dx, float *dweight, float *dbias,
+                              int64_t rows, int64_t channels,
+                              unsigned flags, int dtype, mamba_stream_t stream);
+
 /* How mamba_selective_scan_ex (zero-order hold, default flags) would split a
  * problem (host-side planning only). */
 typedef struct {

@@ -19,6 +19,8 @@
 #include "scan.cuh"
 #include "ssd.cuh"
 #include "complex_scan.cuh"
+#include "gated.cuh"
+#include "norm.cuh"
 
 namespace mamba {
 
@@ -809,6 +811,101 @@ int launch_complex(ComplexArgs a, int64_t batch, int64_t supers_req, cudaStream_
   return st;
 }
 
+
+// --- gated linear recurrence (gated.cuh) --------------------------------------
+// f(element type, log form, convex form) as compile-time constants
+template <typename F>
+int dispatch_gate(int dtype, unsigned flags, F&& f) {
+  auto forms = [&](auto tio) {
+    using T = std::true_type;
+    using N = std::false_type;
+    if (flags & MAMBA_GATE_LOG) return (flags & MAMBA_GATE_CONVEX) ? f(tio, T{}, T{}) : f(tio, T{}, N{});
+    return (flags & MAMBA_GATE_CONVEX) ? f(tio, N{}, T{}) : f(tio, N{}, N{});
+  };
+  return dtype == MAMBA_BF16 ? forms(__nv_bfloat16{}) : forms(float{});
+}
+
+bool gated_size_ok(int64_t batch, int64_t len, int64_t channels) {
+  constexpr int64_t kMax = int64_t(1) << 31;
+  return batch < kMax && len < kMax && channels < kMax && batch * len < kMax && batch * channels < kMax &&
+         batch * len < (kMax << 29) / channels;  // so byte counts fit 64 bits
+}
+
+// Memory an entry point of the gated recurrence or the layer norm reads or
+// writes; their outputs may not overlap anything else of the call (a tile's
+// outputs are written while other tiles still read their inputs).
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+template <size_t NOUT, size_t NIN>
+bool outputs_apart(const Span (&out)[NOUT], const Span (&in)[NIN]) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uint64_t)b.bytes && y < x + (uint64_t)a.bytes;
+  };
+  for (size_t i = 0; i < NOUT; ++i) {
+    for (size_t j = 0; j < NIN; ++j)
+      if (meet(out[i], in[j])) return false;
+    for (size_t j = i + 1; j < NOUT; ++j)
+      if (meet(out[i], out[j])) return false;
+  }
+  return true;
+}
+
+// a [batch][channels] state copied, or zeros where there is none
+int copy_state(float* to, const float* from, int64_t batch, int64_t channels, cudaStream_t stream) {
+  if (!to) return MAMBA_OK;
+  const size_t bytes = sizeof(float) * (size_t)batch * (size_t)channels;
+  const cudaError_t e = from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, stream)
+                             : cudaMemsetAsync(to, 0, bytes, stream);
+  return e == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA;
+}
+
+constexpr int kGatedThreads = 128;
+
+template <typename... K, typename... A>
+int launch_1d(void (*kernel)(K...), int64_t blocks, int threads, cudaStream_t stream, A... a) {
+  if (blocks >= (int64_t(1) << 31)) return MAMBA_ERR_UNSUPPORTED;
+  kernel<<<(unsigned)blocks, threads, 0, stream>>>(a...);
+  return cudaGetLastError() == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA;
+}
+
+int launch_gated(GatedArgs p, bool backward, unsigned flags, int dtype, cudaStream_t stream) {
+  p.blocks = (p.len + kGatedBlock - 1) / kGatedBlock;
+  p.ctiles = (unsigned)((p.channels + kGatedThreads - 1) / kGatedThreads);
+  const size_t maps = (size_t)p.batch * (size_t)p.blocks * (size_t)p.channels;
+  const bool own_ckpt = p.ckpt == nullptr;
+  unsigned char* mem = nullptr;
+  if (scratch_alloc(reinterpret_cast<void**>(&mem),
+                    maps * (sizeof(float2) + 8) + (backward ? 4 * (size_t)p.batch * p.len * p.channels : 0),
+                    stream) != cudaSuccess)
+    return MAMBA_ERR_CUDA;
+  p.agg = reinterpret_cast<float2*>(mem);
+  p.enter = reinterpret_cast<float*>(mem + maps * sizeof(float2));
+  if (own_ckpt) p.ckpt = p.enter + maps;
+  p.hs = backward ? p.enter + 2 * maps : nullptr;
+  const int64_t tiles = p.batch * p.blocks * p.ctiles, rows = (p.batch * p.channels + 127) / 128;
+  int st = dispatch_gate(dtype, flags, [&](auto tio, auto log, auto convex) -> int {
+    using TIO = decltype(tio);
+    constexpr bool L = decltype(log)::value, C = decltype(convex)::value;
+    int e = MAMBA_OK;
+    if (own_ckpt || !backward) {
+      e = launch_1d(gated_block_kernel<TIO, L, C, false>, tiles, kGatedThreads, stream, p);
+      if (e == MAMBA_OK) e = launch_1d(gated_carry_kernel<false>, rows, 128, stream, p);
+    }
+    if (e == MAMBA_OK) e = launch_1d(gated_output_kernel<TIO, L, C>, tiles, kGatedThreads, stream, p);
+    if (e == MAMBA_OK && backward) {
+      e = launch_1d(gated_block_kernel<TIO, L, C, true>, tiles, kGatedThreads, stream, p);
+      if (e == MAMBA_OK) e = launch_1d(gated_carry_kernel<true>, rows, 128, stream, p);
+      if (e == MAMBA_OK) e = launch_1d(gated_gradient_kernel<TIO, L, C>, tiles, kGatedThreads, stream, p);
+    }
+    return e;
+  });
+  if (cudaFreeAsync(mem, stream) != cudaSuccess && st == MAMBA_OK) st = MAMBA_ERR_CUDA;
+  return st;
+}
+
 }  // namespace
 }  // namespace mamba
 
@@ -1362,6 +1459,164 @@ int mamba_selective_scan_complex(const void* u, const void* delta, const float* 
     case 8: return go(std::integral_constant<int, 8>{});
     default: return go(std::integral_constant<int, 16>{});
   }
+}
+
+int mamba_gated_scan(const void* x, const void* gate, const float* initial_state, void* y, float* final_state,
+                     float* checkpoints, int64_t batch, int64_t len, int64_t channels, unsigned flags, int dtype,
+                     mamba_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (dtype != MAMBA_F32 && dtype != MAMBA_BF16) return MAMBA_ERR_INVALID_ARG;
+  if (batch < 0 || len < 0 || channels < 0) return MAMBA_ERR_INVALID_ARG;
+  if (flags & ~(MAMBA_GATE_LOG | MAMBA_GATE_CONVEX)) return MAMBA_ERR_INVALID_ARG;
+  if (batch == 0 || channels == 0) return MAMBA_OK;
+  const size_t es = (size_t)elem_size(dtype);
+  if (len > 0 && (!x || !gate || !y || !aligned(x, es) || !aligned(gate, es) || !aligned(y, es)))
+    return MAMBA_ERR_INVALID_ARG;
+  if (!aligned(initial_state, 4) || !aligned(final_state, 4) || !aligned(checkpoints, 4)) return MAMBA_ERR_INVALID_ARG;
+  if (!gated_size_ok(batch, len, channels)) return MAMBA_ERR_UNSUPPORTED;
+  const int64_t io = batch * len * channels * (int64_t)es, st = batch * channels * 4;
+  const int64_t ck = batch * ((len + kGatedBlock - 1) / kGatedBlock) * channels * 4;
+  if (!outputs_apart({{y, io}, {final_state, st}, {checkpoints, ck}}, {{x, io}, {gate, io}, {initial_state, st}}))
+    return MAMBA_ERR_INVALID_ARG;
+  if (len == 0) return copy_state(final_state, initial_state, batch, channels, stream);
+  GatedArgs p = {};
+  p.x = x;
+  p.gate = gate;
+  p.h0 = initial_state;
+  p.y = y;
+  p.final_state = final_state;
+  p.ckpt = checkpoints;
+  p.batch = batch;
+  p.len = len;
+  p.channels = channels;
+  return launch_gated(p, false, flags, dtype, stream);
+}
+
+int mamba_gated_scan_backward(const void* x, const void* gate, const float* initial_state, const float* checkpoints,
+                              const void* dy, const float* d_final_state, void* dx, void* dgate,
+                              float* d_initial_state, int64_t batch, int64_t len, int64_t channels, unsigned flags,
+                              int dtype, mamba_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (dtype != MAMBA_F32 && dtype != MAMBA_BF16) return MAMBA_ERR_INVALID_ARG;
+  if (batch < 0 || len < 0 || channels < 0) return MAMBA_ERR_INVALID_ARG;
+  if (flags & ~(MAMBA_GATE_LOG | MAMBA_GATE_CONVEX)) return MAMBA_ERR_INVALID_ARG;
+  if (batch == 0 || channels == 0) return MAMBA_OK;
+  const size_t es = (size_t)elem_size(dtype);
+  if (len > 0 && (!x || !gate || !dy || !dx || !dgate || !aligned(x, es) || !aligned(gate, es) || !aligned(dy, es) ||
+                  !aligned(dx, es) || !aligned(dgate, es)))
+    return MAMBA_ERR_INVALID_ARG;
+  if (!aligned(initial_state, 4) || !aligned(checkpoints, 4) || !aligned(d_final_state, 4) ||
+      !aligned(d_initial_state, 4))
+    return MAMBA_ERR_INVALID_ARG;
+  if (!gated_size_ok(batch, len, channels)) return MAMBA_ERR_UNSUPPORTED;
+  const int64_t io = batch * len * channels * (int64_t)es, st = batch * channels * 4;
+  const int64_t ck = batch * ((len + kGatedBlock - 1) / kGatedBlock) * channels * 4;
+  if (!outputs_apart({{dx, io}, {dgate, io}, {d_initial_state, st}},
+                     {{x, io}, {gate, io}, {dy, io}, {initial_state, st}, {checkpoints, ck}, {d_final_state, st}}))
+    return MAMBA_ERR_INVALID_ARG;
+  if (len == 0) return copy_state(d_initial_state, d_final_state, batch, channels, stream);
+  GatedArgs p = {};
+  p.x = x;
+  p.gate = gate;
+  p.dy = dy;
+  p.h0 = initial_state;
+  p.dh = d_final_state;
+  p.ckpt = const_cast<float*>(checkpoints);  // only read by the backward when given
+  p.dx = dx;
+  p.dgate = dgate;
+  p.dh0 = d_initial_state;
+  p.batch = batch;
+  p.len = len;
+  p.channels = channels;
+  return launch_gated(p, true, flags, dtype, stream);
+}
+
+int mamba_gated_step(float* state, const void* x, const void* gate, void* y, int64_t batch, int64_t channels,
+                     unsigned flags, int dtype, mamba_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (dtype != MAMBA_F32 && dtype != MAMBA_BF16) return MAMBA_ERR_INVALID_ARG;
+  if (batch < 0 || channels < 0) return MAMBA_ERR_INVALID_ARG;
+  if (flags & ~(MAMBA_GATE_LOG | MAMBA_GATE_CONVEX)) return MAMBA_ERR_INVALID_ARG;
+  if (batch == 0 || channels == 0) return MAMBA_OK;
+  if (!state || !x || !gate || !y) return MAMBA_ERR_INVALID_ARG;
+  const size_t es = (size_t)elem_size(dtype);
+  if (!aligned(state, 4) || !aligned(x, es) || !aligned(gate, es) || !aligned(y, es)) return MAMBA_ERR_INVALID_ARG;
+  if (!gated_size_ok(batch, 1, channels)) return MAMBA_ERR_UNSUPPORTED;
+  const int64_t io = batch * channels * (int64_t)es;
+  if (!outputs_apart({{state, batch * channels * 4}, {y, io}}, {{x, io}, {gate, io}})) return MAMBA_ERR_INVALID_ARG;
+  return dispatch_gate(dtype, flags, [&](auto tio, auto log, auto convex) -> int {
+    using TIO = decltype(tio);
+    const int64_t n = batch * channels;
+    return launch_1d(gated_step_kernel<TIO, decltype(log)::value, decltype(convex)::value>, (n + 255) / 256, 256, stream,
+              state, static_cast<const TIO*>(x), static_cast<const TIO*>(gate), static_cast<TIO*>(y), n);
+  });
+}
+
+int mamba_layer_norm(const void* x, const float* weight, const float* bias, void* y, float* mean, float* rstd,
+                     int64_t rows, int64_t channels, float eps, unsigned flags, int dtype, mamba_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (dtype != MAMBA_F32 && dtype != MAMBA_BF16) return MAMBA_ERR_INVALID_ARG;
+  if (rows < 0 || channels < 0 || !(eps >= 0.0f) || eps > 3.0e38f) return MAMBA_ERR_INVALID_ARG;
+  if (flags & ~MAMBA_NORM_RMS) return MAMBA_ERR_INVALID_ARG;
+  if (rows == 0 || channels == 0) return MAMBA_OK;
+  const size_t es = (size_t)elem_size(dtype);
+  if (!x || !y || !aligned(x, es) || !aligned(y, es)) return MAMBA_ERR_INVALID_ARG;
+  if (!aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4)) return MAMBA_ERR_INVALID_ARG;
+  if (rows >= (int64_t(1) << 31) || channels > MAMBA_NORM_MAX_CHANNELS) return MAMBA_ERR_UNSUPPORTED;
+  const int64_t io = rows * channels * (int64_t)es;
+  if (!outputs_apart({{y, io}, {mean, 4 * rows}, {rstd, 4 * rows}},
+                     {{x, io}, {weight, 4 * channels}, {bias, 4 * channels}}))
+    return MAMBA_ERR_INVALID_ARG;
+  const int rms = (flags & MAMBA_NORM_RMS) ? 1 : 0;
+  auto run = [&](auto tio) {
+    using TIO = decltype(tio);
+    return launch_1d(norm_kernel<TIO>, rows, 256, stream, static_cast<const TIO*>(x), weight, bias, static_cast<TIO*>(y),
+              mean, rstd, channels, eps, rms);
+  };
+  return dtype == MAMBA_BF16 ? run(__nv_bfloat16{}) : run(float{});
+}
+
+int mamba_layer_norm_backward(const void* dy, const void* x, const float* weight, const float* mean,
+                              const float* rstd, void* dx, float* dweight, float* dbias, int64_t rows,
+                              int64_t channels, unsigned flags, int dtype, mamba_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (dtype != MAMBA_F32 && dtype != MAMBA_BF16) return MAMBA_ERR_INVALID_ARG;
+  if (rows < 0 || channels < 0) return MAMBA_ERR_INVALID_ARG;
+  if (flags & ~MAMBA_NORM_RMS) return MAMBA_ERR_INVALID_ARG;
+  if (channels == 0) return MAMBA_OK;
+  const int rms = (flags & MAMBA_NORM_RMS) ? 1 : 0;
+  const size_t es = (size_t)elem_size(dtype);
+  if (rows > 0 && (!dy || !x || !dx || !rstd || (!rms && !mean) || !aligned(dy, es) || !aligned(x, es) ||
+                   !aligned(dx, es)))
+    return MAMBA_ERR_INVALID_ARG;
+  if (!aligned(weight, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dbias, 4))
+    return MAMBA_ERR_INVALID_ARG;
+  if (rows >= (int64_t(1) << 31) || channels > MAMBA_NORM_MAX_CHANNELS) return MAMBA_ERR_UNSUPPORTED;
+  const int64_t io = rows * channels * (int64_t)es;
+  if (!outputs_apart({{dx, io}, {dweight, 4 * channels}, {dbias, 4 * channels}},
+                     {{dy, io}, {x, io}, {weight, 4 * channels}, {mean, 4 * rows}, {rstd, 4 * rows}}))
+    return MAMBA_ERR_INVALID_ARG;
+  if (rows == 0) {  // empty sums
+    const size_t bytes = sizeof(float) * (size_t)channels;
+    if ((dweight && cudaMemsetAsync(dweight, 0, bytes, stream) != cudaSuccess) ||
+        (dbias && cudaMemsetAsync(dbias, 0, bytes, stream) != cudaSuccess))
+      return MAMBA_ERR_CUDA;
+    return MAMBA_OK;
+  }
+  auto run = [&](auto tio) {
+    using TIO = decltype(tio);
+    const TIO* dyp = static_cast<const TIO*>(dy);
+    const TIO* xp = static_cast<const TIO*>(x);
+    int st = launch_1d(norm_input_gradient_kernel<TIO>, rows, 256, stream, dyp, xp, weight, mean, rstd, static_cast<TIO*>(dx),
+                channels, rms);
+    if (st == MAMBA_OK && (dweight || dbias)) {
+      norm_weight_gradient_kernel<TIO><<<(unsigned)((channels + 31) / 32), dim3(32, 8), 0, stream>>>(
+          dyp, xp, mean, rstd, dweight, dbias, rows, channels, rms);
+      if (cudaGetLastError() != cudaSuccess) st = MAMBA_ERR_CUDA;
+    }
+    return st;
+  };
+  return dtype == MAMBA_BF16 ? run(__nv_bfloat16{}) : run(float{});
 }
 
 int mamba_get_device_error(mamba_stream_t stream_, int clear) {

@@ -25,6 +25,11 @@ MAMBA_ERR_TIMEOUT = 4
 MAMBA_SCAN_GENERAL_A = 1
 MAMBA_SCAN_EULER = 2
 MAMBA_SCAN_TRAPEZOID = 4
+MAMBA_GATE_LOG = 1
+MAMBA_GATE_CONVEX = 2
+MAMBA_GATED_SCAN_BLOCK = 256
+MAMBA_NORM_RMS = 1
+MAMBA_NORM_MAX_CHANNELS = 16384
 
 class ScanPlan(ctypes.Structure):
     """mamba_scan_plan_t"""
@@ -63,6 +68,16 @@ _SIGNATURES = [
     ("mamba_mimo_supported", ctypes.c_int, [_I64, _I64]),
     ("mamba_state_update_mimo", ctypes.c_int,
      [_P] * 8 + [_I64] * 4 + [ctypes.c_int, _P]),
+    ("mamba_gated_scan", ctypes.c_int,
+     [_P] * 6 + [_I64] * 3 + [ctypes.c_uint, ctypes.c_int, _P]),
+    ("mamba_gated_scan_backward", ctypes.c_int,
+     [_P] * 9 + [_I64] * 3 + [ctypes.c_uint, ctypes.c_int, _P]),
+    ("mamba_gated_step", ctypes.c_int,
+     [_P] * 4 + [_I64] * 2 + [ctypes.c_uint, ctypes.c_int, _P]),
+    ("mamba_layer_norm", ctypes.c_int,
+     [_P] * 6 + [_I64] * 2 + [ctypes.c_float, ctypes.c_uint, ctypes.c_int, _P]),
+    ("mamba_layer_norm_backward", ctypes.c_int,
+     [_P] * 8 + [_I64] * 2 + [ctypes.c_uint, ctypes.c_int, _P]),
     ("mamba_scan_plan", ctypes.c_int,
      [_I64, _I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ScanPlan)]),
     ("mamba_status_string", ctypes.c_char_p, [ctypes.c_int]),
@@ -228,6 +243,41 @@ def mamba_state_update_mimo(state, x, delta, A, B, C, D, y, batch, ranks, channe
 
 def mamba_mimo_supported(ranks: int, nstate: int) -> bool:
     return bool(library().mamba_mimo_supported(int(ranks), int(nstate)))
+
+
+def mamba_gated_scan(x, gate, initial_state, y, final_state, checkpoints, batch, len, channels, flags, dtype,
+                     stream=None):
+    st = library().mamba_gated_scan(_ptr(x), _ptr(gate), _ptr(initial_state), _ptr(y), _ptr(final_state),
+                                    _ptr(checkpoints), batch, len, channels, flags, dtype, _stream(stream))
+    _check(st, "mamba_gated_scan")
+
+
+def mamba_gated_scan_backward(x, gate, initial_state, checkpoints, dy, d_final_state, dx, dgate, d_initial_state,
+                              batch, len, channels, flags, dtype, stream=None):
+    st = library().mamba_gated_scan_backward(
+        _ptr(x), _ptr(gate), _ptr(initial_state), _ptr(checkpoints), _ptr(dy), _ptr(d_final_state), _ptr(dx),
+        _ptr(dgate), _ptr(d_initial_state), batch, len, channels, flags, dtype, _stream(stream))
+    _check(st, "mamba_gated_scan_backward")
+
+
+def mamba_gated_step(state, x, gate, y, batch, channels, flags, dtype, stream=None):
+    st = library().mamba_gated_step(_ptr(state), _ptr(x), _ptr(gate), _ptr(y), batch, channels, flags, dtype,
+                                    _stream(stream))
+    _check(st, "mamba_gated_step")
+
+
+def mamba_layer_norm(x, weight, bias, y, mean, rstd, rows, channels, eps, flags, dtype, stream=None):
+    st = library().mamba_layer_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), rows,
+                                    channels, eps, flags, dtype, _stream(stream))
+    _check(st, "mamba_layer_norm")
+
+
+def mamba_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, rows, channels, flags, dtype,
+                              stream=None):
+    st = library().mamba_layer_norm_backward(_ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
+                                             _ptr(dweight), _ptr(dbias), rows, channels, flags, dtype,
+                                             _stream(stream))
+    _check(st, "mamba_layer_norm_backward")
 
 
 def mamba_scan_plan(batch, len, channels, nstate, chunk_len, dtype, sm_count=0) -> ScanPlan:
@@ -432,3 +482,213 @@ def state_update_mimo(state, x, delta, A, B, C, D=None, y=None, stream=None):
         y = torch.empty_like(x)
     mamba_state_update_mimo(state, x, delta, A, B, C, D, y, batch, ranks, channels, nstate, dtype_code(x.dtype), stream)
     return y
+
+
+# --- gated recurrence and layer norm ------------------------------------------------
+
+def _on_stream(x, stream, inputs, call):
+    """call(handle) -> tensors it allocated, made with x's device current and
+    on `stream` (None: that device's current stream).  On another stream than
+    the current one, inputs and results are marked as used on both."""
+    import torch
+    device = x.device
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        caller = torch.cuda.current_stream()
+        if stream is None:
+            return call(caller.cuda_stream)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors of {device}")
+        if stream.cuda_stream == caller.cuda_stream:
+            return call(stream.cuda_stream)
+        with torch.cuda.stream(stream):
+            out = call(stream.cuda_stream)
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        for t in out:
+            if t is not None:
+                t.record_stream(caller)
+        return out
+
+
+def _expect(name, t, shape, dtype, device):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _expect_cuda(name, t, dims):
+    if t.dim() != dims or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dims} dimensions, got {tuple(t.shape)} on "
+                         f"{t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+_GATE_FLAGS = {"sigmoid": 0, "log": MAMBA_GATE_LOG}
+
+
+def gated_scan(x, gate, initial_state=None, return_final_state=True, gate_form="sigmoid", convex=False,
+               checkpoints=None, y=None, final_state=None, stream=None):
+    """y, final_state = the gated recurrence h_t = a_t h_{t-1} + w_t x_t on CUDA tensors.
+
+    x, gate: (batch, len, channels) of one dtype (float32 or bfloat16);
+    gate_form "sigmoid" (a = sigmoid(gate)) or "log" (a = exp(gate)); convex:
+    w = 1 - a instead of 1; initial_state: (batch, channels) float32 or None.
+    checkpoints: None, or a float32 tensor (see gated_scan_checkpoints) that
+    receives the states gated_scan_backward can start from."""
+    import torch
+    _expect_cuda("x", x, 3)
+    shape, dtype, device = x.shape, x.dtype, x.device
+    code = dtype_code(dtype)
+    batch, length, channels = shape
+    rows = (batch, channels)
+    flags = _GATE_FLAGS[gate_form] | (MAMBA_GATE_CONVEX if convex else 0)
+    f32 = torch.float32
+    _expect("gate", gate, shape, dtype, device)
+    if initial_state is not None:
+        _expect("initial_state", initial_state, rows, f32, device)
+    if checkpoints is not None:
+        _expect("checkpoints", checkpoints, (batch, -(-length // MAMBA_GATED_SCAN_BLOCK), channels), f32, device)
+    if y is not None:
+        _expect("y", y, shape, dtype, device)
+    if final_state is not None:
+        _expect("final_state", final_state, rows, f32, device)
+
+    def call(handle):
+        out = torch.empty_like(x) if y is None else y
+        last = final_state
+        if last is None and return_final_state:
+            last = torch.empty(rows, device=device, dtype=f32)
+        mamba_gated_scan(x, gate, initial_state, out, last, checkpoints, batch, length, channels, flags, code, handle)
+        return out, last
+    return _on_stream(x, stream, (x, gate, initial_state, checkpoints), call)
+
+
+def gated_scan_checkpoints(x):
+    """An empty float32 (batch, blocks, channels) tensor for gated_scan's checkpoints."""
+    import torch
+    _expect_cuda("x", x, 3)
+    return torch.empty((x.shape[0], -(-x.shape[1] // MAMBA_GATED_SCAN_BLOCK), x.shape[2]), device=x.device,
+                       dtype=torch.float32)
+
+
+def gated_scan_backward(x, gate, dy, initial_state=None, d_final_state=None, checkpoints=None, gate_form="sigmoid",
+                        convex=False, stream=None):
+    """Gradients of gated_scan for an upstream gradient dy of y (and
+    d_final_state of the final state).  checkpoints: what the forward call
+    with the same x, gate and initial_state wrote, or None (computed again).
+    Returns a dict: dx, dgate (dtype of x), d_initial_state (float32)."""
+    import torch
+    _expect_cuda("x", x, 3)
+    shape, dtype, device = x.shape, x.dtype, x.device
+    code = dtype_code(dtype)
+    batch, length, channels = shape
+    rows = (batch, channels)
+    flags = _GATE_FLAGS[gate_form] | (MAMBA_GATE_CONVEX if convex else 0)
+    f32 = torch.float32
+    _expect("gate", gate, shape, dtype, device)
+    _expect("dy", dy, shape, dtype, device)
+    if initial_state is not None:
+        _expect("initial_state", initial_state, rows, f32, device)
+    if d_final_state is not None:
+        _expect("d_final_state", d_final_state, rows, f32, device)
+    if checkpoints is not None:
+        _expect("checkpoints", checkpoints, (batch, -(-length // MAMBA_GATED_SCAN_BLOCK), channels), f32, device)
+
+    def call(handle):
+        dx, dgate = torch.empty_like(x), torch.empty_like(gate)
+        dh = torch.empty(rows, device=device, dtype=f32)
+        mamba_gated_scan_backward(x, gate, initial_state, checkpoints, dy, d_final_state, dx, dgate, dh, batch,
+                                  length, channels, flags, code, handle)
+        return dx, dgate, dh
+    dx, dgate, dh = _on_stream(x, stream, (x, gate, dy, initial_state, d_final_state, checkpoints), call)
+    return {"dx": dx, "dgate": dgate, "d_initial_state": dh}
+
+
+def gated_step(state, x, gate, gate_form="sigmoid", convex=False, y=None, stream=None):
+    """One token of the gated recurrence in place on `state` (batch, channels)
+    float32; x, gate: (batch, channels).  Returns y in the dtype of x."""
+    import torch
+    _expect_cuda("x", x, 2)
+    shape, dtype, device = x.shape, x.dtype, x.device
+    code = dtype_code(dtype)
+    _expect("gate", gate, shape, dtype, device)
+    _expect("state", state, shape, torch.float32, device)
+    if y is not None:
+        _expect("y", y, shape, dtype, device)
+    flags = _GATE_FLAGS[gate_form] | (MAMBA_GATE_CONVEX if convex else 0)
+
+    def call(handle):
+        out = torch.empty_like(x) if y is None else y
+        mamba_gated_step(state, x, gate, out, shape[0], shape[1], flags, code, handle)
+        return (out,)
+    return _on_stream(x, stream, (x, gate, state), call)[0]
+
+
+def _norm_rows(x):
+    if x.dim() == 0 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"x: expected a contiguous CUDA tensor of rows, got {tuple(x.shape)} on {x.device}")
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    return rows, x.shape[-1]
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, y=None, stream=None):
+    """y, mean, rstd = layer norm of x (..., channels) over its last dimension.
+
+    x: float32 or bfloat16; weight, bias: (channels,) float32 or None; rms:
+    no mean is taken off (mean is then zero).  mean, rstd: x.shape[:-1]
+    float32, for layer_norm_backward."""
+    import torch
+    rows, channels = _norm_rows(x)
+    dtype, device = x.dtype, x.device
+    code = dtype_code(dtype)
+    f32 = torch.float32
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _expect(name, t, (channels,), f32, device)
+    if y is not None:
+        _expect("y", y, x.shape, dtype, device)
+
+    def call(handle):
+        out = torch.empty_like(x) if y is None else y
+        mean = torch.empty(x.shape[:-1], device=device, dtype=f32)
+        rstd = torch.empty(x.shape[:-1], device=device, dtype=f32)
+        mamba_layer_norm(x, weight, bias, out, mean, rstd, rows, channels, eps, MAMBA_NORM_RMS if rms else 0, code,
+                         handle)
+        return out, mean, rstd
+    return _on_stream(x, stream, (x, weight, bias), call)
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, rms=False, stream=None):
+    """Gradients of layer_norm for an upstream gradient dy, with the mean and
+    rstd the forward call returned.  Returns a dict: dx (dtype of x), dweight
+    (None without a weight), dbias (None with bias=False), float32."""
+    import torch
+    rows, channels = _norm_rows(x)
+    dtype, device = x.dtype, x.device
+    code = dtype_code(dtype)
+    f32 = torch.float32
+    _expect("dy", dy, x.shape, dtype, device)
+    if weight is not None:
+        _expect("weight", weight, (channels,), f32, device)
+    if mean is not None or not rms:
+        _expect("mean", mean, x.shape[:-1], f32, device)
+    _expect("rstd", rstd, x.shape[:-1], f32, device)
+
+    def call(handle):
+        dx = torch.empty_like(x)
+        dw = None if weight is None else torch.empty((channels,), device=device, dtype=f32)
+        db = torch.empty((channels,), device=device, dtype=f32) if bias else None
+        mamba_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db, rows, channels,
+                                  MAMBA_NORM_RMS if rms else 0, code, handle)
+        return dx, dw, db
+    dx, dw, db = _on_stream(x, stream, (dy, x, weight, mean, rstd), call)
+    return {"dx": dx, "dweight": dw, "dbias": db}
