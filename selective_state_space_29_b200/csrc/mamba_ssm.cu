@@ -862,8 +862,6 @@ int copy_state(float* to, const float* from, int64_t batch, int64_t channels, cu
   return e == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA;
 }
 
-constexpr int kGatedThreads = 128;
-
 template <typename... K, typename... A>
 int launch_1d(void (*kernel)(K...), int64_t blocks, int threads, cudaStream_t stream, A... a) {
   if (blocks >= (int64_t(1) << 31)) return MAMBA_ERR_UNSUPPORTED;
@@ -871,38 +869,86 @@ int launch_1d(void (*kernel)(K...), int64_t blocks, int threads, cudaStream_t st
   return cudaGetLastError() == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA;
 }
 
-int launch_gated(GatedArgs p, bool backward, unsigned flags, int dtype, cudaStream_t stream) {
-  p.blocks = (p.len + kGatedBlock - 1) / kGatedBlock;
-  p.ctiles = (unsigned)((p.channels + kGatedThreads - 1) / kGatedThreads);
-  const size_t maps = (size_t)p.batch * (size_t)p.blocks * (size_t)p.channels;
-  const bool own_ckpt = p.ckpt == nullptr;
-  unsigned char* mem = nullptr;
-  if (scratch_alloc(reinterpret_cast<void**>(&mem),
-                    maps * (sizeof(float2) + 8) + (backward ? 4 * (size_t)p.batch * p.len * p.channels : 0),
-                    stream) != cudaSuccess)
+// One pass over every tile: the forward kernel, or the backward one.  rec and
+// ticket are scratch of gated_scratch_bytes for this pass, or NULL.
+template <typename TIO, bool LOG, bool CONVEX, bool BACKWARD, int CB>
+int launch_gated_pass(const GatedArgs& p, cudaStream_t stream) {
+  int sms = 0;
+  if (int st = current_sms(&sms)) return st;
+  constexpr int kBytes =
+      BACKWARD ? GatedSmem<TIO>::bwd(kGatedBwdStages) : GatedSmem<TIO>::fwd(kGatedFwdStages);
+  auto kernel = [] {
+    if constexpr (BACKWARD) return gated_backward_kernel<TIO, LOG, CONVEX, CB>;
+    else return gated_scan_kernel<TIO, LOG, CONVEX, CB>;
+  }();
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
     return MAMBA_ERR_CUDA;
-  p.agg = reinterpret_cast<float2*>(mem);
-  p.enter = reinterpret_cast<float*>(mem + maps * sizeof(float2));
-  if (own_ckpt) p.ckpt = p.enter + maps;
-  p.hs = backward ? p.enter + 2 * maps : nullptr;
-  const int64_t tiles = p.batch * p.blocks * p.ctiles, rows = (p.batch * p.channels + 127) / 128;
-  int st = dispatch_gate(dtype, flags, [&](auto tio, auto log, auto convex) -> int {
-    using TIO = decltype(tio);
-    constexpr bool L = decltype(log)::value, C = decltype(convex)::value;
-    int e = MAMBA_OK;
-    if (own_ckpt || !backward) {
-      e = launch_1d(gated_block_kernel<TIO, L, C, false>, tiles, kGatedThreads, stream, p);
-      if (e == MAMBA_OK) e = launch_1d(gated_carry_kernel<false>, rows, 128, stream, p);
+  const unsigned ctas = (unsigned)std::min<int64_t>(p.jobs, 2 * (int64_t)sms);
+  return launch_pdl(kernel, dim3(ctas), dim3(kGatedThreads), (size_t)kBytes, stream, p) == cudaSuccess ? MAMBA_OK
+                                                                                                    : MAMBA_ERR_CUDA;
+}
+
+int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int dtype, cudaStream_t stream) {
+  const int64_t es = elem_size(dtype), chan = kGatedRow / es;
+  const int64_t blocks = (p.len + kGatedBlock - 1) / kGatedBlock, groups = (p.channels + chan - 1) / chan;
+  if (batch * groups >= (int64_t(1) << 31) || batch * groups * blocks >= (int64_t(1) << 31) - (1 << 20))
+    return MAMBA_ERR_UNSUPPORTED;
+  p.blocks = (int)blocks;
+  p.groups = (int)groups;
+  p.chains = (int)(batch * groups);
+  p.jobs = (int)(batch * groups * blocks);
+  p.wait_limit_ns = kWaitLimitNs;
+  // what a copy moves: 16 or 4 bytes where every tensor and every row of
+  // channels is aligned to them, else single elements
+  auto all_aligned = [&](size_t a) {
+    return (p.channels * es) % (int64_t)a == 0 && aligned(p.x, a) && aligned(p.gate, a) && aligned(p.dy, a) &&
+           aligned(p.y, a) && aligned(p.dx, a) && aligned(p.dgate, a);
+  };
+  const int cb = all_aligned(16) ? 16 : all_aligned(4) ? 4 : 2;
+  // scratch: records and a counter for every pass over several tiles of time,
+  // and the checkpoints that a backward call has not been given
+  const bool own_ckpt = backward && !p.ckpt;
+  const size_t pass = blocks > 1 ? ((size_t)p.jobs * chan + 2) * sizeof(unsigned long long) : 0;
+  const size_t passes = pass * (own_ckpt ? 2 : 1);
+  const size_t ck = own_ckpt ? (size_t)batch * blocks * p.channels * sizeof(float) : 0;
+  unsigned char* mem = nullptr;
+  if (passes + ck > 0 && scratch_alloc(reinterpret_cast<void**>(&mem), passes + ck, stream) != cudaSuccess)
+    return MAMBA_ERR_CUDA;
+  int st = MAMBA_OK;
+  // records not yet written, counters one before the first tile
+  if (passes > 0 && cudaMemsetAsync(mem, 0xff, passes, stream) != cudaSuccess) st = MAMBA_ERR_CUDA;
+  auto scratch_of = [&](GatedArgs q, int i) {
+    if (pass > 0) {
+      q.ticket = reinterpret_cast<int*>(mem + i * pass);
+      q.rec = reinterpret_cast<unsigned long long*>(mem + i * pass) + 2;
     }
-    if (e == MAMBA_OK) e = launch_1d(gated_output_kernel<TIO, L, C>, tiles, kGatedThreads, stream, p);
-    if (e == MAMBA_OK && backward) {
-      e = launch_1d(gated_block_kernel<TIO, L, C, true>, tiles, kGatedThreads, stream, p);
-      if (e == MAMBA_OK) e = launch_1d(gated_carry_kernel<true>, rows, 128, stream, p);
-      if (e == MAMBA_OK) e = launch_1d(gated_gradient_kernel<TIO, L, C>, tiles, kGatedThreads, stream, p);
-    }
-    return e;
-  });
-  if (cudaFreeAsync(mem, stream) != cudaSuccess && st == MAMBA_OK) st = MAMBA_ERR_CUDA;
+    return q;
+  };
+  auto run = [&](auto cbc) {
+    constexpr int CB = decltype(cbc)::value;
+    return dispatch_gate(dtype, flags, [&](auto tio, auto log, auto convex) -> int {
+      using TIO = decltype(tio);
+      constexpr bool L = decltype(log)::value, C = decltype(convex)::value;
+      if constexpr (CB == 2 && sizeof(TIO) == 4) {
+        return MAMBA_ERR_INVALID_ARG;  // float32 tensors are 4-byte aligned
+      } else {
+        if (!backward) return launch_gated_pass<TIO, L, C, false, CB>(scratch_of(p, 0), stream);
+        int e = MAMBA_OK;
+        GatedArgs q = scratch_of(p, 0);
+        if (own_ckpt) {
+          q.ckpt = reinterpret_cast<float*>(mem + passes);
+          GatedArgs f = scratch_of(q, 1);
+          f.y = nullptr;
+          e = launch_gated_pass<TIO, L, C, false, CB>(f, stream);
+        }
+        return e == MAMBA_OK ? launch_gated_pass<TIO, L, C, true, CB>(q, stream) : e;
+      }
+    });
+  };
+  if (st == MAMBA_OK)
+    st = cb == 16 ? run(std::integral_constant<int, 16>{})
+                  : cb == 4 ? run(std::integral_constant<int, 4>{}) : run(std::integral_constant<int, 2>{});
+  if (mem && cudaFreeAsync(mem, stream) != cudaSuccess && st == MAMBA_OK) st = MAMBA_ERR_CUDA;
   return st;
 }
 
@@ -1486,10 +1532,9 @@ int mamba_gated_scan(const void* x, const void* gate, const float* initial_state
   p.y = y;
   p.final_state = final_state;
   p.ckpt = checkpoints;
-  p.batch = batch;
   p.len = len;
   p.channels = channels;
-  return launch_gated(p, false, flags, dtype, stream);
+  return launch_gated(p, batch, false, flags, dtype, stream);
 }
 
 int mamba_gated_scan_backward(const void* x, const void* gate, const float* initial_state, const float* checkpoints,
@@ -1525,10 +1570,9 @@ int mamba_gated_scan_backward(const void* x, const void* gate, const float* init
   p.dx = dx;
   p.dgate = dgate;
   p.dh0 = d_initial_state;
-  p.batch = batch;
   p.len = len;
   p.channels = channels;
-  return launch_gated(p, true, flags, dtype, stream);
+  return launch_gated(p, batch, true, flags, dtype, stream);
 }
 
 int mamba_gated_step(float* state, const void* x, const void* gate, void* y, int64_t batch, int64_t channels,
