@@ -952,6 +952,81 @@ int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int 
   return st;
 }
 
+// --- layer norm (norm.cuh) -----------------------------------------------------
+// f(element type, elements per vector): 16-byte vectors where every tensor and
+// every row is aligned to them, else single elements
+template <typename F>
+int dispatch_norm(int dtype, bool vec, F&& f) {
+  using One = std::integral_constant<int, 1>;
+  if (dtype == MAMBA_BF16)
+    return vec ? f(__nv_bfloat16{}, std::integral_constant<int, 8>{}) : f(__nv_bfloat16{}, One{});
+  return vec ? f(float{}, std::integral_constant<int, 4>{}) : f(float{}, One{});
+}
+
+// lanes per row (log2, 4 to 512 lanes) that hold `vecs` vectors at `per` each
+int norm_lanes_log2(int64_t vecs, int64_t per) {
+  int l = 2;
+  while ((int64_t(1) << l) * per < vecs && l < 9) ++l;
+  return l;
+}
+
+template <typename TIO, int E>
+int launch_norm(NormArgs p, cudaStream_t stream) {
+  int sms = 0;
+  if (int st = current_sms(&sms)) return st;
+  const int64_t vecs = (p.channels + E - 1) / E;
+  auto run = [&](auto vpl) -> int {
+    constexpr int VPL = decltype(vpl)::value;
+    p.lr_log2 = norm_lanes_log2(vecs, VPL);
+    const int threads = std::max(256, 1 << p.lr_log2);
+    const int64_t slots = threads >> p.lr_log2, ctas = (p.rows + slots - 1) / slots;
+    return launch_pdl(norm_kernel<TIO, E, VPL>, dim3((unsigned)ctas), dim3(threads), 0, stream, p) == cudaSuccess
+               ? MAMBA_OK
+               : MAMBA_ERR_CUDA;
+  };
+  constexpr int K = E == 1 ? 4 : 1;  // single elements: four times the vectors a lane
+  // the most vectors a lane that still leave the SMs 1,024 lanes each
+  auto fills = [&](int per) { return (p.rows << norm_lanes_log2(vecs, per)) >= (int64_t)sms * 1024; };
+  if (vecs > 4 * K * 512 || fills(8 * K)) return run(std::integral_constant<int, 8 * K>{});
+  if (vecs > 2 * K * 512 || fills(4 * K)) return run(std::integral_constant<int, 4 * K>{});
+  return run(std::integral_constant<int, 2 * K>{});
+}
+
+template <typename TIO, int E>
+int launch_norm_backward(NormArgs p, cudaStream_t stream) {
+  int sms = 0;
+  if (int st = current_sms(&sms)) return st;
+  const int64_t vecs = (p.channels + E - 1) / E;
+  auto run = [&](auto vpl) -> int {
+    constexpr int VPL = decltype(vpl)::value;
+    p.lr_log2 = norm_lanes_log2(vecs, VPL);
+    const int threads = kNormMaxThreads;
+    const int64_t slots = threads >> p.lr_log2;
+    const int ctas = (int)std::min<int64_t>(sms, (p.rows + slots - 1) / slots);
+    const size_t smem = (size_t)threads * VPL * E * sizeof(float);
+    auto kernel = norm_backward_kernel<TIO, E, VPL>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return MAMBA_ERR_CUDA;
+    unsigned char* mem = nullptr;
+    if (p.dweight || p.dbias) {
+      if (scratch_alloc(reinterpret_cast<void**>(&mem), (size_t)ctas * 2 * p.channels * sizeof(float), stream) !=
+          cudaSuccess)
+        return MAMBA_ERR_CUDA;
+      p.part = reinterpret_cast<float*>(mem);
+    }
+    int st = launch_pdl(kernel, dim3(ctas), dim3(threads), smem, stream, p) == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA;
+    if (st == MAMBA_OK && mem &&
+        launch_pdl(norm_join_kernel, dim3((unsigned)((p.channels + 31) / 32), 2), dim3(32, 32), 0, stream, p, ctas) !=
+            cudaSuccess)
+      st = MAMBA_ERR_CUDA;
+    if (mem && cudaFreeAsync(mem, stream) != cudaSuccess && st == MAMBA_OK) st = MAMBA_ERR_CUDA;
+    return st;
+  };
+  // a lane holds 16 elements (32 in the longest rows)
+  if (vecs * E > 16 * kNormMaxThreads) return run(std::integral_constant<int, 32 / E>{});
+  return run(std::integral_constant<int, 16 / E>{});
+}
+
 }  // namespace
 }  // namespace mamba
 
@@ -1611,13 +1686,22 @@ int mamba_layer_norm(const void* x, const float* weight, const float* bias, void
   if (!outputs_apart({{y, io}, {mean, 4 * rows}, {rstd, 4 * rows}},
                      {{x, io}, {weight, 4 * channels}, {bias, 4 * channels}}))
     return MAMBA_ERR_INVALID_ARG;
-  const int rms = (flags & MAMBA_NORM_RMS) ? 1 : 0;
-  auto run = [&](auto tio) {
-    using TIO = decltype(tio);
-    return launch_1d(norm_kernel<TIO>, rows, 256, stream, static_cast<const TIO*>(x), weight, bias, static_cast<TIO*>(y),
-              mean, rstd, channels, eps, rms);
-  };
-  return dtype == MAMBA_BF16 ? run(__nv_bfloat16{}) : run(float{});
+  NormArgs p = {};
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.y = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.rows = rows;
+  p.channels = (int)channels;
+  p.wide = aligned(weight, 16) && aligned(bias, 16);
+  p.rms = (flags & MAMBA_NORM_RMS) ? 1 : 0;
+  p.eps = eps;
+  const bool vec = (channels * (int64_t)es) % 16 == 0 && aligned(x, 16) && aligned(y, 16);
+  return dispatch_norm(dtype, vec, [&](auto tio, auto e) {
+    return launch_norm<decltype(tio), decltype(e)::value>(p, stream);
+  });
 }
 
 int mamba_layer_norm_backward(const void* dy, const void* x, const float* weight, const float* mean,
@@ -1647,20 +1731,23 @@ int mamba_layer_norm_backward(const void* dy, const void* x, const float* weight
       return MAMBA_ERR_CUDA;
     return MAMBA_OK;
   }
-  auto run = [&](auto tio) {
-    using TIO = decltype(tio);
-    const TIO* dyp = static_cast<const TIO*>(dy);
-    const TIO* xp = static_cast<const TIO*>(x);
-    int st = launch_1d(norm_input_gradient_kernel<TIO>, rows, 256, stream, dyp, xp, weight, mean, rstd, static_cast<TIO*>(dx),
-                channels, rms);
-    if (st == MAMBA_OK && (dweight || dbias)) {
-      norm_weight_gradient_kernel<TIO><<<(unsigned)((channels + 31) / 32), dim3(32, 8), 0, stream>>>(
-          dyp, xp, mean, rstd, dweight, dbias, rows, channels, rms);
-      if (cudaGetLastError() != cudaSuccess) st = MAMBA_ERR_CUDA;
-    }
-    return st;
-  };
-  return dtype == MAMBA_BF16 ? run(__nv_bfloat16{}) : run(float{});
+  NormArgs p = {};
+  p.x = x;
+  p.dy = dy;
+  p.weight = weight;
+  p.y = dx;
+  p.mean_in = mean;
+  p.rstd_in = rstd;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  p.rows = rows;
+  p.channels = (int)channels;
+  p.wide = aligned(weight, 16);
+  p.rms = rms;
+  const bool vec = (channels * (int64_t)es) % 16 == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(dx, 16);
+  return dispatch_norm(dtype, vec, [&](auto tio, auto e) {
+    return launch_norm_backward<decltype(tio), decltype(e)::value>(p, stream);
+  });
 }
 
 int mamba_get_device_error(mamba_stream_t stream_, int clear) {
