@@ -37,6 +37,8 @@
 // the states that enter every block of 256 tokens (checkpoints).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace mamba {
@@ -72,19 +74,23 @@ struct GatedArgs {
   int groups;            // channel groups
   int chains;            // batch * groups
   int jobs;              // chains * blocks
+  unsigned rcp_chains, rcp_groups;  // floor(2^32 / ...), for divisions
   uint64_t wait_limit_ns;
 };
 
 // ---------------------------------------------------------------------------
-// gates
+// gates, two at a time (packed fp32 instructions)
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float rcp_newton(float d) {
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float2 rcp_newton(float2 d) {
   // hardware reciprocal (1 ulp) and one Newton step: within 2^-24 of 1/d.  The
   // step is taken for bf16 data too: a state remembers thousands of gates, and
   // an error of one sign in each adds up in the float32 states.
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
-  return fmaf(r, fmaf(-d, r, 1.0f), r);
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  return __ffma2_rn(r, __ffma2_rn(make_float2(-d.x, -d.y), r, both(1.0f)), r);
 }
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
@@ -92,56 +98,99 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
-// a and 1 - a of a gate.  FAST (bf16 data): hardware exp2 (2^-22 of its value);
-// else the CUDA library's functions.  Sigmoid: with e = exp(-g), a = 1/(1 + e)
-// and 1 - a = e a, which has no cancellation; below g = -87, where e would
-// overflow, a is zero.  Log form: near zero exp(g) - 1 by its series (next
-// term below 2^-22 of it), which also keeps the bias of exp2 next to one out
-// of long memories.
-template <bool LOG, bool FAST>
-__device__ __forceinline__ void gate_decay(float g, float& a, float& one_less) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  if constexpr (!LOG) {
-    const float t = min_nan(FAST ? g * -kLog2e : -g, FAST ? 126.0f : 87.0f);
-    const float e = FAST ? ex2_approx(t) : expf(t);
-    const float r = rcp_newton(1.0f + e);
-    one_less = e * r;
-    a = t >= (FAST ? 126.0f : 87.0f) ? 0.0f : r;
-  } else if constexpr (FAST) {
-    const float big = ex2_approx(g * kLog2e);
-    float p = fmaf(g, 1.0f / 720.0f, 1.0f / 120.0f);
-    p = fmaf(p, g, 1.0f / 24.0f);
-    p = fmaf(p, g, 1.0f / 6.0f);
-    p = fmaf(p, g, 0.5f);
-    p = fmaf(p, g, 1.0f);
-    const bool small = fabsf(g) < 0.3f;
-    a = small ? fmaf(g, p, 1.0f) : big;
-    one_less = small ? -g * p : 1.0f - big;
+// exp(-g) of the sigmoid, at most kGateTop: there 1 / (1 + e) is 1 / kGateTop
+// exactly, which is taken off again, so that a gate of minus infinity gives a
+// = 0 and 1 - a = 1 exactly (a gate above is moved by 2^-125).  FAST (bf16
+// data): hardware exp2, 2^-22 of its value; else the CUDA library's.
+constexpr float kGateTop = 42535295865117307932921825928971026432.0f;  // 2^125
+constexpr float kGateTopRcp = 2.350988701644575e-38f;                  // 2^-125
+template <bool FAST>
+__device__ __forceinline__ float2 gate_exp_neg(float2 g) {
+  if constexpr (FAST) {
+    const float2 t = __fmul2_rn(g, both(-1.4426950408889634f));
+    return make_float2(min_nan(ex2_approx(t.x), kGateTop), min_nan(ex2_approx(t.y), kGateTop));
   } else {
-    a = expf(g);
-    one_less = -expm1f(g);
+    return make_float2(min_nan(expf(-g.x), kGateTop), min_nan(expf(-g.y), kGateTop));
   }
 }
 
-// 4 bytes of channels as floats
+// exp(g) - 1 near zero by its series (the next term is below 2^-22 of it for |g| < 0.3)
+__device__ __forceinline__ float2 expm1_series(float2 g) {
+  float2 p = __ffma2_rn(g, both(1.0f / 720.0f), both(1.0f / 120.0f));
+  p = __ffma2_rn(p, g, both(1.0f / 24.0f));
+  p = __ffma2_rn(p, g, both(1.0f / 6.0f));
+  p = __ffma2_rn(p, g, both(0.5f));
+  p = __ffma2_rn(p, g, both(1.0f));
+  return __fmul2_rn(p, g);
+}
+
+// a and 1 - a of two gates.  Sigmoid: with e = exp(-g), a = 1/(1 + e) and 1 -
+// a = e a, which has no cancellation.  Log form, FAST: near zero by the
+// series, which also keeps the bias of exp2 next to one out of long memories.
+template <bool LOG, bool FAST>
+__device__ __forceinline__ void gate_decay(float2 g, float2& a, float2& one_less) {
+  if constexpr (!LOG) {
+    const float2 e = gate_exp_neg<FAST>(g);
+    const float2 r = rcp_newton(__fadd2_rn(e, both(1.0f)));
+    one_less = __fmul2_rn(e, r);
+    a = __fadd2_rn(r, both(-kGateTopRcp));
+  } else if constexpr (FAST) {
+    const float2 t = __fmul2_rn(g, both(1.4426950408889634f));
+    const float2 big = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+    const float2 m = expm1_series(g);
+    const float2 near = __fadd2_rn(m, both(1.0f)), rest = __fadd2_rn(make_float2(-big.x, -big.y), both(1.0f));
+    const bool sx = fabsf(g.x) < 0.3f, sy = fabsf(g.y) < 0.3f;
+    a = make_float2(sx ? near.x : big.x, sy ? near.y : big.y);
+    one_less = make_float2(sx ? -m.x : rest.x, sy ? -m.y : rest.y);
+  } else {
+    a = make_float2(expf(g.x), expf(g.y));
+    one_less = make_float2(-expm1f(g.x), -expm1f(g.y));
+  }
+}
+// 1 - a again, where a is still at hand
+template <bool LOG, bool FAST>
+__device__ __forceinline__ float2 gate_one_less(float2 g, float2 a) {
+  if constexpr (!LOG) {
+    return __fmul2_rn(gate_exp_neg<FAST>(g), __fadd2_rn(a, both(kGateTopRcp)));
+  } else {
+    float2 again, w;
+    gate_decay<LOG, FAST>(g, again, w);
+    return w;
+  }
+}
+
+// A lane's 4 bytes of channels: two bf16 channels, or one float32.  Values are
+// worked on in pairs: the two channels of a token, or two tokens of the channel.
 template <typename TIO>
 struct Lane4 {
-  static constexpr int kV = 4 / (int)sizeof(TIO);
-  static __device__ __forceinline__ void get(uint32_t w, float (&v)[kV]) {
+  static constexpr int kV = 4 / (int)sizeof(TIO);  // channels
+  static constexpr int kWords = 2 / kV;            // words (tokens) of a pair
+  static __device__ __forceinline__ float2 get(const uint32_t (&w)[kWords]) {
+    if constexpr (kV == 1) return make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    else return make_float2(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void put(float2 v, uint32_t (&w)[kWords]) {
     if constexpr (kV == 1) {
-      v[0] = __uint_as_float(w);
+      w[0] = __float_as_uint(v.x);
+      w[1] = __float_as_uint(v.y);
     } else {
-      v[0] = __uint_as_float(w << 16);
-      v[1] = __uint_as_float(w & 0xffff0000u);
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[0]) : "f"(v.y), "f"(v.x));
     }
   }
-  static __device__ __forceinline__ uint32_t put(const float (&v)[kV]) {
-    if constexpr (kV == 1) {
-      return __float_as_uint(v[0]);
+  // h <- a h + b over a pair; h.y is unused where the pair is two tokens
+  static __device__ __forceinline__ void step(float2 a, float2 b, float2& h) {
+    if constexpr (kV == 2) h = __ffma2_rn(a, h, b);
+    else h.x = fmaf(a.y, fmaf(a.x, h.x, b.x), b.y);
+  }
+  // the state before and after every token of a pair
+  static __device__ __forceinline__ void walk(float2 a, float2 b, float2& h, float2& before, float2& after) {
+    if constexpr (kV == 2) {
+      before = h;
+      after = h = __ffma2_rn(a, h, b);
     } else {
-      uint32_t w;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(v[1]), "f"(v[0]));
-      return w;
+      before.x = h.x;
+      before.y = after.x = fmaf(a.x, h.x, b.x);
+      after.y = h.x = fmaf(a.y, before.y, b.y);
     }
   }
 };
@@ -165,17 +214,29 @@ __device__ __forceinline__ void gated_copy(uint32_t dst, const unsigned char* sr
 // rows [0, n) x bytes [0, width) of a tile whose first byte is src
 template <int CB>
 __device__ __forceinline__ void gated_load(uint32_t dst, const unsigned char* src, int64_t pitch, int n, int width) {
-  constexpr int kPer = kGatedRow / CB;                            // copies per row
-  constexpr int kRows = kGatedThreads / kPer;                     // rows per round
-  const int col = (threadIdx.x % kPer) * CB, r0 = threadIdx.x / kPer;
+  constexpr int kPer = kGatedRow / CB;         // copies per row
+  constexpr int kRows = kGatedThreads / kPer;  // rows per round
+  const int col = ((int)threadIdx.x % kPer) * CB, r0 = (int)threadIdx.x / kPer;
   if (col >= width) return;
   src += r0 * pitch + col;
+  dst += (r0 / kGatedTok) * kGatedSegBytes + (r0 % kGatedTok) * kGatedRow + col;
+  auto at = [&](int i) {  // of row r0 + i kRows
+    if constexpr (kRows >= kGatedTok) return dst + i * (kRows / kGatedTok) * kGatedSegBytes;
+    else return dst + (i / (kGatedTok / kRows)) * kGatedSegBytes + (i % (kGatedTok / kRows)) * kRows * kGatedRow;
+  };
+  static_assert(kRows >= kGatedTok ? kRows % kGatedTok == 0 : kGatedTok % kRows == 0, "whole segments");
+  if (n == kGatedBlock) {
 #pragma unroll(CB == 16 ? 4 : 8)
-  for (int i = 0; i < kGatedBlock / kRows; ++i) {
-    const int r = r0 + i * kRows;
-    if (r < n)
-      gated_copy<CB>(dst + (r / kGatedTok) * kGatedSegBytes + (r % kGatedTok) * kGatedRow + col, src);
-    src += kRows * pitch;
+    for (int i = 0; i < kGatedBlock / kRows; ++i) {
+      gated_copy<CB>(at(i), src);
+      src += kRows * pitch;
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < kGatedBlock / kRows && r0 + i * kRows < n; ++i) {
+      gated_copy<CB>(at(i), src);
+      src += kRows * pitch;
+    }
   }
 }
 
@@ -251,60 +312,131 @@ __device__ __forceinline__ float gated_look_back(const unsigned long long* own, 
   }
 }
 
-// Tile `job` of a launch: chain (batch row, channel group) and time block.
-struct GatedTile {
-  int64_t at;   // element index of its first token's first channel
-  int k, chain; // block counted in walking order, chain
-  int c0;       // first channel
-  int b;
-  int n;        // tokens
+// Tile of a launch: chain (batch row, channel group) and time block.
+struct __align__(16) GatedTile {
+  int64_t at;    // element index of its first token's first channel
+  int job;       // jobs or more: no tile
+  int k;         // block, counted in walking order
+  int chain, b;  // chain, batch row
+  int c0;        // first channel
+  int n;         // tokens
 };
+__device__ __forceinline__ int gated_div(int n, int d, unsigned rcp) {
+  int q = (int)__umulhi((unsigned)n, rcp);  // at most one too small
+  if (n - q * d >= d) ++q;
+  return q;
+}
 template <typename TIO, bool REVERSE>
-__device__ __forceinline__ GatedTile gated_tile(const GatedArgs& p, int job) {
-  GatedTile t;
-  t.k = job / p.chains;
-  t.chain = job - t.k * p.chains;
-  t.b = t.chain / p.groups;
-  t.c0 = (t.chain - t.b * p.groups) * (kGatedRow / (int)sizeof(TIO));
-  const int block = REVERSE ? p.blocks - 1 - t.k : t.k;
-  const int64_t t0 = (int64_t)block * kGatedBlock;
-  t.n = (int)min((int64_t)kGatedBlock, p.len - t0);
-  t.at = ((int64_t)t.b * p.len + t0) * p.channels + t.c0;
-  return t;
+__device__ __forceinline__ void gated_tile(const GatedArgs& p, int job, GatedTile* to) {
+  GatedTile t = {};
+  t.job = job;
+  if (job < p.jobs) {
+    t.k = gated_div(job, p.chains, p.rcp_chains);
+    t.chain = job - t.k * p.chains;
+    t.b = gated_div(t.chain, p.groups, p.rcp_groups);
+    t.c0 = (t.chain - t.b * p.groups) * (kGatedRow / (int)sizeof(TIO));
+    const int block = REVERSE ? p.blocks - 1 - t.k : t.k;
+    const int64_t t0 = (int64_t)block * kGatedBlock;
+    t.n = (int)min((int64_t)kGatedBlock, p.len - t0);
+    t.at = ((int64_t)t.b * p.len + t0) * p.channels + t.c0;
+  }
+  *to = t;
 }
 
-// Shared memory: the stages, then the segments' maps and entering states.
-template <typename TIO>
+constexpr int kGatedStages = 2;
+
+// Shared memory: the stages, the segments' maps (one float per segment and
+// channel each), what enters the tile, the stages' tiles.
+template <typename TIO, bool BACKWARD>
 struct GatedSmem {
   static constexpr int kChan = kGatedRow / (int)sizeof(TIO);
-  static constexpr int kSmall = kGatedSegs * kChan * 4;  // one float per segment and channel
-  static constexpr int fwd(int stages) { return stages * 2 * kGatedStream + 3 * kSmall + 64; }
-  static constexpr int bwd(int stages) { return stages * 3 * kGatedStream + 5 * kSmall + 64; }
+  static constexpr int kStage = (BACKWARD ? 3 : 2) * kGatedStream;
+  static constexpr int kMap = kGatedSegs * kChan * 4;
+  static constexpr int kMaps = kGatedStages * kStage;
+  static constexpr int kEnter = kMaps + (BACKWARD ? 3 : 2) * kMap;
+  static constexpr int kTiles = kEnter + 2 * kChan * 4;
+  static constexpr int kFlag = kTiles + kGatedStages * (int)sizeof(GatedTile);
+  static constexpr int kBytes = kFlag + 16;
 };
-constexpr int kGatedFwdStages = 2;
-constexpr int kGatedBwdStages = 2;
 
-// Tiles of a CTA: S to start with, then one for each that is done.  With one
-// tile per CTA at most, each takes just one, so that none waits behind another.
-// One tile per chain: no order is needed, and tiles are dealt by block index.
-template <int S>
-__device__ __forceinline__ void gated_first(const GatedArgs& p, int* queue) {
-  if (threadIdx.x != 0) return;
-  const bool ahead = p.jobs > (int)gridDim.x;
-  int first = blockIdx.x, step = gridDim.x;
-  if (p.ticket) {
-    first = atomicAdd(p.ticket, ahead ? S : 1) + 1;
-    step = ahead ? 1 : p.jobs;
-  }
-  queue[0] = first;
-#pragma unroll
-  for (int s = 1; s < S; ++s) queue[s] = min(first + s * step, p.jobs);
-}
-template <int S>
+// Tiles of a CTA: one per stage and one more held, each taken by itself, so
+// that the first ones of all CTAs come before anyone's second (a tile's map is
+// published only once the CTA's earlier tiles are done).  With one tile per CTA
+// at most, each takes just one.  One tile per chain: no order is needed, and
+// tiles are dealt by block index.
 __device__ __forceinline__ int gated_next(const GatedArgs& p, int job) {
-  if (p.jobs <= (int)gridDim.x) return p.jobs;
-  return p.ticket ? atomicAdd(p.ticket, 1) + 1 : min(job + S * (int)gridDim.x, p.jobs);
+  if (job >= 0 && p.jobs <= (int)gridDim.x) return p.jobs;
+  if (p.ticket) return atomicAdd(p.ticket, 1) + 1;
+  return job < 0 ? (int)blockIdx.x : min(job + (int)gridDim.x, p.jobs);
 }
+
+// The tile's map from its segments', in walking order
+template <int CHAN, bool REVERSE>
+__device__ __forceinline__ void gated_fold(const float* seg_p, const float* seg_h, int ch, float& tp, float& th) {
+  tp = 1.0f;
+  th = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kGatedSegs; ++i) {
+    const int s = REVERSE ? kGatedSegs - 1 - i : i;
+    const float sp = seg_p[s * CHAN + ch];
+    th = fmaf(sp, th, seg_h[s * CHAN + ch]);
+    tp *= sp;
+  }
+}
+
+// A lane's channels of a plane of maps or of what enters
+template <int V>
+__device__ __forceinline__ float2 gated_pair(const float* p) {
+  if constexpr (V == 2) return *reinterpret_cast<const float2*>(p);
+  else return make_float2(*p, 0.0f);
+}
+
+// What enters this lane's segment: through the `count` segments before it in
+// walking order, from `h`, what enters the tile
+template <int V, int CHAN, bool REVERSE>
+__device__ __forceinline__ float2 gated_enter(const float* seg_p, const float* seg_h, int count, float2 h) {
+  auto through = [&](int i) {
+    const int s = REVERSE ? kGatedSegs - 1 - i : i;
+    const float2 sp = gated_pair<V>(seg_p + s * CHAN), sh = gated_pair<V>(seg_h + s * CHAN);
+    if constexpr (V == 2) h = __ffma2_rn(sp, h, sh);
+    else h.x = fmaf(sp.x, h.x, sh.x);
+  };
+  // two segments share a warp: the pairs before it, then the odd one
+#pragma unroll 2
+  for (int i = 0; i + 1 < count; i += 2) {
+    through(i);
+    through(i + 1);
+  }
+  if (count & 1) through(count - 1);
+  return h;
+}
+
+// One direction's carry, for warp 0 with a lane per channel.  peek: before the
+// tile's map is known, what entered if that is known already; publish: the
+// map, and later what leaves the tile.
+struct GatedCarry {
+  unsigned long long* rec;
+  int64_t stride;
+  unsigned long long seen;
+  float value;
+  bool active;
+  __device__ __forceinline__ void peek(const GatedArgs& p, const GatedTile& t, int chan, const float* start) {
+    const int lane = threadIdx.x;
+    active = lane < chan && t.c0 + lane < p.channels;
+    stride = (int64_t)p.chains * chan;
+    rec = p.rec + (int64_t)t.k * stride + t.chain * chan + (active ? lane : 0);
+    value = 0.0f;
+    seen = 0ull;
+    if (active && t.k > 0) seen = rec_get(rec - stride);
+    if (active && t.k == 0 && start) value = start[(int64_t)t.b * p.channels + t.c0 + lane];
+  }
+  // whether what enters is known in every lane
+  __device__ __forceinline__ bool known(const GatedTile& t) {
+    const uint32_t pb = (uint32_t)(seen >> 32);
+    if (t.k > 0) value = __uint_as_float((uint32_t)seen);
+    return __all_sync(0xffffffffu, !active || pb == 0u || pb == 0x80000000u);
+  }
+};
 
 // ---------------------------------------------------------------------------
 // forward
@@ -312,126 +444,131 @@ __device__ __forceinline__ int gated_next(const GatedArgs& p, int job) {
 template <typename TIO, bool LOG, bool CONVEX, int CB>
 __global__ void __launch_bounds__(kGatedThreads, 2) gated_scan_kernel(const GatedArgs p) {
   using L4 = Lane4<TIO>;
-  constexpr int V = L4::kV, kChan = GatedSmem<TIO>::kChan, kES = (int)sizeof(TIO), S = kGatedFwdStages;
+  using SM = GatedSmem<TIO, false>;
+  constexpr int V = L4::kV, W = L4::kWords, kChan = SM::kChan, kES = (int)sizeof(TIO), kPairs = kGatedTok / W;
   extern __shared__ __align__(16) unsigned char smem[];
-  float* seg_p = reinterpret_cast<float*>(smem + S * 2 * kGatedStream);  // [segment][channel]
+  float* seg_p = reinterpret_cast<float*>(smem + SM::kMaps);  // [segment][channel]
   float* seg_h = seg_p + kGatedSegs * kChan;
-  float* seg_in = seg_h + kGatedSegs * kChan;
-  int* queue = reinterpret_cast<int*>(seg_in + kGatedSegs * kChan);
-  const int tid = threadIdx.x, seg = tid >> 4, sl = tid & 15;
-  const uint32_t stage0 = smem_addr(smem);
-  const uint32_t mine = seg * kGatedSegBytes + sl * 4;
+  float* enter = reinterpret_cast<float*>(smem + SM::kEnter);
+  GatedTile* tiles = reinterpret_cast<GatedTile*>(smem + SM::kTiles);
+  int* flag = reinterpret_cast<int*>(smem + SM::kFlag);
+  const int tid = threadIdx.x, seg = tid >> 4, col = (tid & 15) * V;
+  const uint32_t stage0 = smem_addr(smem), mine = seg * kGatedSegBytes + (tid & 15) * 4;
   const int64_t pitch = p.channels * kES;
   griddep_launch_dependents();
   griddep_wait();
 
-  // several tiles per CTA: one is worked on while the next is loaded
-  gated_first<S>(p, queue);
-  __syncthreads();
+  int held = -1;  // thread 32: the tile after those of the stages
   auto load = [&](int stage) {
-    const int job = queue[stage];
-    if (job < p.jobs) {
-      const GatedTile t = gated_tile<TIO, false>(p, job);
+    const GatedTile& t = tiles[stage];
+    if (t.job < p.jobs) {
       const int width = (int)min((int64_t)kGatedRow, (p.channels - t.c0) * kES);
-      const uint32_t to = stage0 + stage * 2 * kGatedStream;
+      const uint32_t to = stage0 + stage * SM::kStage;
       gated_load<CB>(to, static_cast<const unsigned char*>(p.gate) + t.at * kES, pitch, t.n, width);
       gated_load<CB>(to + kGatedStream, static_cast<const unsigned char*>(p.x) + t.at * kES, pitch, t.n, width);
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < S; ++s) load(s);
-
-  for (int stage = 0;; stage = stage + 1 == S ? 0 : stage + 1) {
-    const int job = queue[stage];
-    if (job >= p.jobs) break;
-    const GatedTile t = gated_tile<TIO, false>(p, job);
-    cp_async_wait<S - 1>();
+  for (int s = 0; s < kGatedStages; ++s) {
+    if (tid == 32) gated_tile<TIO, false>(p, held = gated_next(p, held), tiles + s);
     __syncthreads();
-    int next = 0;
-    if (tid == 32) next = gated_next<S>(p, job);
+    load(s);
+  }
+  if (tid == 32) held = gated_next(p, held);
+
+  for (int stage = 0;; stage = stage + 1 == kGatedStages ? 0 : stage + 1) {
+    const GatedTile t = tiles[stage];
+    if (t.job >= p.jobs) break;
+    cp_async_wait<kGatedStages - 1>();
+    __syncthreads();
+    GatedCarry carry;
+    if (tid < 32) carry.peek(p, t, kChan, p.h0);
 
     // the segment's gates and inputs, and its map
-    const uint32_t from = stage0 + stage * 2 * kGatedStream + mine;
-    const int n = min(kGatedTok, t.n - seg * kGatedTok);
-    float a[kGatedTok][V], b[kGatedTok][V], P[V], H[V];
+    const uint32_t from = stage0 + stage * SM::kStage + mine;
+    const int n = t.n - seg * kGatedTok;
+    float2 a[kPairs], b[kPairs], P = both(1.0f), H = both(0.0f);
+    auto map = [&](auto full) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) P[v] = 1.0f, H[v] = 0.0f;
+      for (int i = 0; i < kPairs; ++i) {
+        uint32_t gw[W], xw[W];
 #pragma unroll
-    for (int i = 0; i < kGatedTok; ++i) {
-      float g[V], x[V], w;
-      L4::get(lds32(from + i * kGatedRow), g);
-      L4::get(lds32(from + kGatedStream + i * kGatedRow), x);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        gate_decay<LOG, sizeof(TIO) == 2>(g[v], a[i][v], w);
-        b[i][v] = CONVEX ? w * x[v] : x[v];
-        if (i < n) {
-          H[v] = fmaf(a[i][v], H[v], b[i][v]);
-          P[v] *= a[i][v];
+        for (int k = 0; k < W; ++k) {
+          gw[k] = lds32(from + (i * W + k) * kGatedRow);
+          xw[k] = lds32(from + kGatedStream + (i * W + k) * kGatedRow);
         }
+        float2 w;
+        gate_decay<LOG, kES == 2>(L4::get(gw), a[i], w);
+        b[i] = CONVEX ? __fmul2_rn(w, L4::get(xw)) : L4::get(xw);
+        if (!decltype(full)::value) {  // tokens after the last leave everything as it is
+          if (i * W >= n) a[i].x = 1.0f, b[i].x = 0.0f;
+          if (i * W + W - 1 >= n) a[i].y = 1.0f, b[i].y = 0.0f;
+        }
+        L4::step(a[i], b[i], H);
+        if constexpr (V == 2) P = __fmul2_rn(P, a[i]);
+        else P.x *= a[i].x, P.x *= a[i].y;
       }
+    };
+    if (t.n == kGatedBlock) map(std::true_type{});
+    else map(std::false_type{});
+    if constexpr (V == 2) {
+      *reinterpret_cast<float2*>(seg_p + seg * kChan + col) = P;
+      *reinterpret_cast<float2*>(seg_h + seg * kChan + col) = H;
+    } else {
+      seg_p[seg * kChan + col] = P.x;
+      seg_h[seg * kChan + col] = H.x;
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      seg_p[seg * kChan + sl * V + v] = P[v];
-      seg_h[seg * kChan + sl * V + v] = H[v];
+    if (tid < 32) {
+      const bool known = carry.known(t);
+      if (tid < kChan) enter[tid] = carry.value;
+      if (tid == 0) *flag = known;
+    } else if (tid == 32) {
+      gated_tile<TIO, false>(p, held, tiles + stage);
+      held = gated_next(p, held);
     }
-    if (tid == 32) queue[stage] = next;
     __syncthreads();
     load(stage);
 
+    const bool known = *flag != 0;
     if (tid < 32) {
-      const bool active = tid < kChan && t.c0 + tid < p.channels;
       const int ch = tid < kChan ? tid : 0;
-      unsigned long long* rec = p.rec + ((int64_t)t.k * p.chains + t.chain) * kChan + ch;
-      const int64_t state_at = (int64_t)t.b * p.channels + t.c0 + ch;
-      float h = 0.0f;
-      if (t.k == 0) {
-        if (active && p.h0) h = p.h0[state_at];
-      } else {
-        float tp = 1.0f, th = 0.0f;
-#pragma unroll
-        for (int s = 0; s < kGatedSegs; ++s) {
-          th = fmaf(seg_p[s * kChan + ch], th, seg_h[s * kChan + ch]);
-          tp *= seg_p[s * kChan + ch];
-        }
-        if (active && t.k + 1 < p.blocks) rec_put(rec, tp, th);
-        h = gated_look_back(rec, t.k, (int64_t)p.chains * kChan, active, p.wait_limit_ns);
+      float tp, th;
+      gated_fold<kChan, false>(seg_p, seg_h, ch, tp, th);
+      const bool more = carry.active && t.k + 1 < p.blocks;
+      if (!known) {
+        if (more) rec_put(carry.rec, tp, th);
+        carry.value = gated_look_back(carry.rec, t.k, carry.stride, carry.active, p.wait_limit_ns);
+        if (tid < kChan) enter[tid] = carry.value;
       }
-      if (active && p.ckpt) p.ckpt[((int64_t)t.b * p.blocks + t.k) * p.channels + t.c0 + ch] = h;
-      // the next tile's entering state, rounded as a reader of (P, H) rounds it
-      float tp = 1.0f, th = 0.0f;
-      const float h_in = h;
-#pragma unroll
-      for (int s = 0; s < kGatedSegs; ++s) {
-        const float sp = seg_p[s * kChan + ch], sh = seg_h[s * kChan + ch];
-        if (tid < kChan) seg_in[s * kChan + ch] = h;
-        h = fmaf(sp, h, sh);
-        th = fmaf(sp, th, sh);
-        tp *= sp;
-      }
-      const float after = fmaf(tp, h_in, th);
-      if (active) {
-        if (t.k + 1 < p.blocks) rec_put(rec, 0.0f, after);
-        else if (p.final_state) p.final_state[state_at] = after;
+      // what leaves, rounded as a reader of (P, H) rounds it
+      const float after = fmaf(tp, carry.value, th);
+      if (more) rec_put(carry.rec, 0.0f, after);
+      if (carry.active) {
+        if (p.ckpt) p.ckpt[((int64_t)t.b * p.blocks + t.k) * p.channels + t.c0 + ch] = carry.value;
+        if (t.k + 1 == p.blocks && p.final_state) p.final_state[(int64_t)t.b * p.channels + t.c0 + ch] = after;
       }
     }
-    __syncthreads();
+    if (!known) __syncthreads();
 
-    if (p.y && t.c0 + sl * V < p.channels) {
-      float h[V];
+    if (p.y && t.c0 + col < p.channels) {
+      float2 h = gated_enter<V, kChan, false>(seg_p + col, seg_h + col, seg, gated_pair<V>(enter + col));
+      unsigned char* y = static_cast<unsigned char*>(p.y) + (t.at + (int64_t)seg * kGatedTok * p.channels + col) * kES;
+      const int left = (int)min((int64_t)4, (p.channels - t.c0 - col) * kES);
+      auto out = [&](auto full) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = seg_in[seg * kChan + sl * V + v];
-      unsigned char* y = static_cast<unsigned char*>(p.y) + (t.at + (int64_t)seg * kGatedTok * p.channels + sl * V) * kES;
-      const int left = (int)min((int64_t)4, (p.channels - t.c0 - sl * V) * kES);
+        for (int i = 0; i < kPairs; ++i) {
+          float2 before, after;
+          uint32_t w[W];
+          L4::walk(a[i], b[i], h, before, after);
+          L4::put(after, w);
 #pragma unroll
-      for (int i = 0; i < kGatedTok; ++i) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], b[i][v]);
-        if (i < n) gated_store<CB>(y, L4::put(h), left);
-        y += pitch;
-      }
+          for (int k = 0; k < W; ++k)
+            if (decltype(full)::value || i * W + k < n) gated_store<CB>(y + (i * W + k) * pitch, w[k], left);
+        }
+      };
+      if (t.n == kGatedBlock) out(std::true_type{});
+      else out(std::false_type{});
     }
   }
 }
@@ -444,30 +581,29 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_scan_kernel(const Gate
 template <typename TIO, bool LOG, bool CONVEX, int CB>
 __global__ void __launch_bounds__(kGatedThreads, 2) gated_backward_kernel(const GatedArgs p) {
   using L4 = Lane4<TIO>;
-  constexpr int V = L4::kV, kChan = GatedSmem<TIO>::kChan, kES = (int)sizeof(TIO), S = kGatedBwdStages;
-  constexpr bool kFast = sizeof(TIO) == 2;
+  using SM = GatedSmem<TIO, true>;
+  constexpr int V = L4::kV, W = L4::kWords, kChan = SM::kChan, kES = (int)sizeof(TIO), kPairs = kGatedTok / W;
+  constexpr bool kFast = kES == 2;
   extern __shared__ __align__(16) unsigned char smem[];
-  float* seg_p = reinterpret_cast<float*>(smem + S * 3 * kGatedStream);  // [segment][channel]
+  float* seg_p = reinterpret_cast<float*>(smem + SM::kMaps);  // [segment][channel]
   float* seg_h = seg_p + kGatedSegs * kChan;
   float* seg_r = seg_h + kGatedSegs * kChan;
-  float* seg_in = seg_r + kGatedSegs * kChan;   // state entering from the left
-  float* seg_adj = seg_in + kGatedSegs * kChan; // adjoint entering from the right
-  int* queue = reinterpret_cast<int*>(seg_adj + kGatedSegs * kChan);
-  const int tid = threadIdx.x, seg = tid >> 4, sl = tid & 15;
-  const uint32_t stage0 = smem_addr(smem);
-  const uint32_t mine = seg * kGatedSegBytes + sl * 4;
+  float* enter = reinterpret_cast<float*>(smem + SM::kEnter);  // adjoint, from the right
+  float* enter_h = enter + kChan;                              // state, from the left
+  GatedTile* tiles = reinterpret_cast<GatedTile*>(smem + SM::kTiles);
+  int* flag = reinterpret_cast<int*>(smem + SM::kFlag);
+  const int tid = threadIdx.x, seg = tid >> 4, col = (tid & 15) * V;
+  const uint32_t stage0 = smem_addr(smem), mine = seg * kGatedSegBytes + (tid & 15) * 4;
   const int64_t pitch = p.channels * kES;
   griddep_launch_dependents();
   griddep_wait();
 
-  gated_first<S>(p, queue);
-  __syncthreads();
+  int held = -1;
   auto load = [&](int stage) {
-    const int job = queue[stage];
-    if (job < p.jobs) {
-      const GatedTile t = gated_tile<TIO, true>(p, job);
+    const GatedTile& t = tiles[stage];
+    if (t.job < p.jobs) {
       const int width = (int)min((int64_t)kGatedRow, (p.channels - t.c0) * kES);
-      const uint32_t to = stage0 + stage * 3 * kGatedStream;
+      const uint32_t to = stage0 + stage * SM::kStage;
       gated_load<CB>(to, static_cast<const unsigned char*>(p.gate) + t.at * kES, pitch, t.n, width);
       gated_load<CB>(to + kGatedStream, static_cast<const unsigned char*>(p.x) + t.at * kES, pitch, t.n, width);
       gated_load<CB>(to + 2 * kGatedStream, static_cast<const unsigned char*>(p.dy) + t.at * kES, pitch, t.n, width);
@@ -475,138 +611,163 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_backward_kernel(const 
     cp_async_commit();
   };
 #pragma unroll
-  for (int s = 0; s < S; ++s) load(s);
-
-  for (int stage = 0;; stage = stage + 1 == S ? 0 : stage + 1) {
-    const int job = queue[stage];
-    if (job >= p.jobs) break;
-    const GatedTile t = gated_tile<TIO, true>(p, job);
-    cp_async_wait<S - 1>();
+  for (int s = 0; s < kGatedStages; ++s) {
+    if (tid == 32) gated_tile<TIO, true>(p, held = gated_next(p, held), tiles + s);
     __syncthreads();
-    int next = 0;
-    if (tid == 32) next = gated_next<S>(p, job);
+    load(s);
+  }
+  if (tid == 32) held = gated_next(p, held);
 
-    const uint32_t from = stage0 + stage * 3 * kGatedStream + mine;
-    const int n = min(kGatedTok, t.n - seg * kGatedTok);
-    float a[kGatedTok][V], b[kGatedTok][V], P[V], H[V], R[V];
+  for (int stage = 0;; stage = stage + 1 == kGatedStages ? 0 : stage + 1) {
+    const GatedTile t = tiles[stage];
+    if (t.job >= p.jobs) break;
+    cp_async_wait<kGatedStages - 1>();
+    __syncthreads();
+    GatedCarry carry;
+    float state = 0.0f;
+    if (tid < 32) carry.peek(p, t, kChan, p.dh);
+    if (tid >= 64 && tid < 64 + kChan && t.c0 + tid - 64 < p.channels)
+      state = p.ckpt[((int64_t)t.b * p.blocks + p.blocks - 1 - t.k) * p.channels + t.c0 + tid - 64];
+
+    const uint32_t from = stage0 + stage * SM::kStage + mine;
+    const int n = t.n - seg * kGatedTok;
+    float2 a[kPairs], b[kPairs], P = both(1.0f), H = both(0.0f), R = both(0.0f);
+    auto map = [&](auto full) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) P[v] = 1.0f, H[v] = 0.0f, R[v] = 0.0f;
+      for (int i = 0; i < kPairs; ++i) {
+        uint32_t gw[W], xw[W], dw[W];
 #pragma unroll
-    for (int i = 0; i < kGatedTok; ++i) {
-      float g[V], x[V], dy[V], w;
-      L4::get(lds32(from + i * kGatedRow), g);
-      L4::get(lds32(from + kGatedStream + i * kGatedRow), x);
-      L4::get(lds32(from + 2 * kGatedStream + i * kGatedRow), dy);
+        for (int k = 0; k < W; ++k) {
+          gw[k] = lds32(from + (i * W + k) * kGatedRow);
+          xw[k] = lds32(from + kGatedStream + (i * W + k) * kGatedRow);
+          dw[k] = lds32(from + 2 * kGatedStream + (i * W + k) * kGatedRow);
+        }
+        float2 w, dy = L4::get(dw);
+        gate_decay<LOG, kFast>(L4::get(gw), a[i], w);
+        b[i] = CONVEX ? __fmul2_rn(w, L4::get(xw)) : L4::get(xw);
+        if (!decltype(full)::value) {
+          if (i * W >= n) a[i].x = 1.0f, b[i].x = 0.0f, dy.x = 0.0f;
+          if (i * W + W - 1 >= n) a[i].y = 1.0f, b[i].y = 0.0f, dy.y = 0.0f;
+        }
+        L4::step(a[i], b[i], H);
+        if constexpr (V == 2) {
+          P = __fmul2_rn(P, a[i]);
+          R = __ffma2_rn(dy, P, R);
+        } else {
+          P.x *= a[i].x;
+          R.x = fmaf(dy.x, P.x, R.x);
+          P.x *= a[i].y;
+          R.x = fmaf(dy.y, P.x, R.x);
+        }
+      }
+    };
+    if (t.n == kGatedBlock) map(std::true_type{});
+    else map(std::false_type{});
+    if constexpr (V == 2) {
+      *reinterpret_cast<float2*>(seg_p + seg * kChan + col) = P;
+      *reinterpret_cast<float2*>(seg_h + seg * kChan + col) = H;
+      *reinterpret_cast<float2*>(seg_r + seg * kChan + col) = R;
+    } else {
+      seg_p[seg * kChan + col] = P.x;
+      seg_h[seg * kChan + col] = H.x;
+      seg_r[seg * kChan + col] = R.x;
+    }
+    if (tid < 32) {
+      const bool known = carry.known(t);
+      if (tid < kChan) enter[tid] = carry.value;
+      if (tid == 0) *flag = known;
+    } else if (tid == 32) {
+      gated_tile<TIO, true>(p, held, tiles + stage);
+      held = gated_next(p, held);
+    }
+    if (tid >= 64 && tid < 64 + kChan) enter_h[tid - 64] = state;
+    __syncthreads();
+
+    const bool known = *flag != 0;
+    if (tid < 32) {
+      const int ch = tid < kChan ? tid : 0;
+      float tp, tr;
+      gated_fold<kChan, true>(seg_p, seg_r, ch, tp, tr);
+      const bool more = carry.active && t.k + 1 < p.blocks;
+      if (!known) {
+        if (more) rec_put(carry.rec, tp, tr);
+        carry.value = gated_look_back(carry.rec, t.k, carry.stride, carry.active, p.wait_limit_ns);
+        if (tid < kChan) enter[tid] = carry.value;
+      }
+      const float after = fmaf(tp, carry.value, tr);
+      if (more) rec_put(carry.rec, 0.0f, after);
+      if (carry.active && t.k + 1 == p.blocks && p.dh0) p.dh0[(int64_t)t.b * p.channels + t.c0 + ch] = after;
+    }
+
+    // b becomes h_{t-1} (minus x_t when convex)
+    const bool mine_live = t.c0 + col < p.channels;
+    {
+      float2 h = gated_enter<V, kChan, false>(seg_p + col, seg_h + col, seg, gated_pair<V>(enter_h + col));
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        gate_decay<LOG, kFast>(g[v], a[i][v], w);
-        b[i][v] = CONVEX ? w * x[v] : x[v];
-        if (i < n) {
-          H[v] = fmaf(a[i][v], H[v], b[i][v]);
-          P[v] *= a[i][v];
-          R[v] = fmaf(dy[v], P[v], R[v]);
+      for (int i = 0; i < kPairs; ++i) {
+        float2 before, after;
+        L4::walk(a[i], b[i], h, before, after);
+        if (CONVEX) {
+          uint32_t xw[W];
+#pragma unroll
+          for (int k = 0; k < W; ++k) xw[k] = lds32(from + kGatedStream + (i * W + k) * kGatedRow);
+          const float2 x = L4::get(xw);
+          b[i] = __fadd2_rn(before, make_float2(-x.x, -x.y));
+        } else {
+          b[i] = before;
         }
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      seg_p[seg * kChan + sl * V + v] = P[v];
-      seg_h[seg * kChan + sl * V + v] = H[v];
-      seg_r[seg * kChan + sl * V + v] = R[v];
-    }
-    __syncthreads();
+    if (!known) __syncthreads();
 
-    const int lane = tid & 31;
-    const bool active = lane < kChan && t.c0 + lane < p.channels;
-    const int ch = lane < kChan ? lane : 0;
-    const int64_t state_at = (int64_t)t.b * p.channels + t.c0 + ch;
-    if (tid < 32) {  // the adjoint, from the right
-      unsigned long long* rec = p.rec + ((int64_t)t.k * p.chains + t.chain) * kChan + ch;
-      float c = 0.0f;
-      if (t.k == 0) {
-        if (active && p.dh) c = p.dh[state_at];
-      } else {
-        float tp = 1.0f, tr = 0.0f;
+    if (mine_live) {
+      float2 c = gated_enter<V, kChan, true>(seg_p + col, seg_r + col, kGatedSegs - 1 - seg, gated_pair<V>(enter + col));
+      const int64_t at = (t.at + (int64_t)seg * kGatedTok * p.channels + col) * kES;
+      unsigned char* dx = static_cast<unsigned char*>(p.dx) + at;
+      unsigned char* dg = static_cast<unsigned char*>(p.dgate) + at;
+      const int left = (int)min((int64_t)4, (p.channels - t.c0 - col) * kES);
+      auto out = [&](auto full) {
 #pragma unroll
-        for (int s = kGatedSegs - 1; s >= 0; --s) {
-          tr = fmaf(seg_p[s * kChan + ch], tr, seg_r[s * kChan + ch]);
-          tp *= seg_p[s * kChan + ch];
-        }
-        if (active && t.k + 1 < p.blocks) rec_put(rec, tp, tr);
-        c = gated_look_back(rec, t.k, (int64_t)p.chains * kChan, active, p.wait_limit_ns);
-      }
-      float tp = 1.0f, tr = 0.0f;
-      const float c_in = c;
+        for (int i = kPairs - 1; i >= 0; --i) {
+          uint32_t gw[W], dw[W], ow[W];
 #pragma unroll
-      for (int s = kGatedSegs - 1; s >= 0; --s) {
-        const float sp = seg_p[s * kChan + ch], sr = seg_r[s * kChan + ch];
-        if (lane < kChan) seg_adj[s * kChan + ch] = c;
-        c = fmaf(sp, c, sr);
-        tr = fmaf(sp, tr, sr);
-        tp *= sp;
-      }
-      const float after = fmaf(tp, c_in, tr);
-      if (active) {
-        if (t.k + 1 < p.blocks) rec_put(rec, 0.0f, after);
-        else if (p.dh0) p.dh0[state_at] = after;
-      }
-    } else if (tid < 64) {  // the states, from the checkpoint
-      const int block = p.blocks - 1 - t.k;
-      float h = active ? p.ckpt[((int64_t)t.b * p.blocks + block) * p.channels + t.c0 + ch] : 0.0f;
-#pragma unroll
-      for (int s = 0; s < kGatedSegs; ++s) {
-        if (lane < kChan) seg_in[s * kChan + ch] = h;
-        h = fmaf(seg_p[s * kChan + ch], h, seg_h[s * kChan + ch]);
-      }
-    }
-    __syncthreads();
-
-    if (t.c0 + sl * V < p.channels) {
-      // b becomes h_{t-1} (minus x_t when convex)
-      float h[V], c[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = seg_in[seg * kChan + sl * V + v];
-        c[v] = seg_adj[seg * kChan + sl * V + v];
-      }
-#pragma unroll
-      for (int i = 0; i < kGatedTok; ++i) {
-        float x[V];
-        if (CONVEX) L4::get(lds32(from + kGatedStream + i * kGatedRow), x);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float before = h[v];
-          h[v] = fmaf(a[i][v], h[v], b[i][v]);
-          b[i][v] = CONVEX ? before - x[v] : before;
-        }
-      }
-      const int64_t at = (t.at + (int64_t)seg * kGatedTok * p.channels + sl * V) * kES;
-      unsigned char* dx = static_cast<unsigned char*>(p.dx) + at + (kGatedTok - 1) * pitch;
-      unsigned char* dg = static_cast<unsigned char*>(p.dgate) + at + (kGatedTok - 1) * pitch;
-      const int left = (int)min((int64_t)4, (p.channels - t.c0 - sl * V) * kES);
-#pragma unroll
-      for (int i = kGatedTok - 1; i >= 0; --i) {
-        if (i < n) {
-          float g[V], dy[V], ox[V], og[V];
-          if (CONVEX || !LOG) L4::get(lds32(from + i * kGatedRow), g);
-          L4::get(lds32(from + 2 * kGatedStream + i * kGatedRow), dy);
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            float again, w = 1.0f;
-            if (CONVEX || !LOG) gate_decay<LOG, kFast>(g[v], again, w);
-            const float lam = dy[v] + c[v];
-            c[v] = a[i][v] * lam;
-            ox[v] = CONVEX ? w * lam : lam;
-            og[v] = (LOG ? c[v] : c[v] * w) * b[i][v];
+          for (int k = 0; k < W; ++k) {
+            if (CONVEX || !LOG) gw[k] = lds32(from + (i * W + k) * kGatedRow);
+            dw[k] = lds32(from + 2 * kGatedStream + (i * W + k) * kGatedRow);
           }
-          gated_store<CB>(dx, L4::put(ox), left);
-          gated_store<CB>(dg, L4::put(og), left);
+          float2 dy = L4::get(dw), lam, back;  // back: a lam
+          if (!decltype(full)::value) {
+            if (i * W >= n) dy.x = 0.0f;
+            if (i * W + W - 1 >= n) dy.y = 0.0f;
+          }
+          if constexpr (V == 2) {
+            lam = __fadd2_rn(dy, c);
+            back = c = __fmul2_rn(a[i], lam);
+          } else {
+            lam.y = dy.y + c.x;
+            back.y = a[i].y * lam.y;
+            lam.x = dy.x + back.y;
+            back.x = c.x = a[i].x * lam.x;
+          }
+          float2 g_out = __fmul2_rn(back, b[i]), x_out = lam;
+          if (CONVEX || !LOG) {
+            const float2 w = gate_one_less<LOG, kFast>(L4::get(gw), a[i]);
+            if (!LOG) g_out = __fmul2_rn(g_out, w);
+            if (CONVEX) x_out = __fmul2_rn(lam, w);
+          }
+          L4::put(x_out, ow);
+#pragma unroll
+          for (int k = 0; k < W; ++k)
+            if (decltype(full)::value || i * W + k < n) gated_store<CB>(dx + (i * W + k) * pitch, ow[k], left);
+          L4::put(g_out, ow);
+#pragma unroll
+          for (int k = 0; k < W; ++k)
+            if (decltype(full)::value || i * W + k < n) gated_store<CB>(dg + (i * W + k) * pitch, ow[k], left);
         }
-        dx -= pitch;
-        dg -= pitch;
-      }
+      };
+      if (t.n == kGatedBlock) out(std::true_type{});
+      else out(std::false_type{});
     }
-    if (tid == 32) queue[stage] = next;
     __syncthreads();  // the stage is read to the end
     load(stage);
   }
@@ -617,10 +778,10 @@ template <typename TIO, bool LOG, bool CONVEX>
 __global__ void gated_step_kernel(float* state, const TIO* x, const TIO* gate, TIO* y, int64_t n) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= n) return;
-  float a, w;
-  gate_decay<LOG, sizeof(TIO) == 2>(to_f32(gate[i]), a, w);
+  float2 a, w;
+  gate_decay<LOG, sizeof(TIO) == 2>(both(to_f32(gate[i])), a, w);
   const float in = to_f32(x[i]);
-  const float h = fmaf(a, state[i], CONVEX ? w * in : in);
+  const float h = fmaf(a.x, state[i], CONVEX ? w.x * in : in);
   state[i] = h;
   y[i] = from_f32<TIO>(h);
 }

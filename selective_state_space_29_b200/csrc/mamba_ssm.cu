@@ -875,8 +875,7 @@ template <typename TIO, bool LOG, bool CONVEX, bool BACKWARD, int CB>
 int launch_gated_pass(const GatedArgs& p, cudaStream_t stream) {
   int sms = 0;
   if (int st = current_sms(&sms)) return st;
-  constexpr int kBytes =
-      BACKWARD ? GatedSmem<TIO>::bwd(kGatedBwdStages) : GatedSmem<TIO>::fwd(kGatedFwdStages);
+  constexpr int kBytes = GatedSmem<TIO, BACKWARD>::kBytes;
   auto kernel = [] {
     if constexpr (BACKWARD) return gated_backward_kernel<TIO, LOG, CONVEX, CB>;
     else return gated_scan_kernel<TIO, LOG, CONVEX, CB>;
@@ -897,6 +896,8 @@ int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int 
   p.groups = (int)groups;
   p.chains = (int)(batch * groups);
   p.jobs = (int)(batch * groups * blocks);
+  p.rcp_chains = (unsigned)std::min<uint64_t>(0xffffffffu, (uint64_t(1) << 32) / (uint64_t)p.chains);
+  p.rcp_groups = (unsigned)std::min<uint64_t>(0xffffffffu, (uint64_t(1) << 32) / (uint64_t)p.groups);
   p.wait_limit_ns = kWaitLimitNs;
   // what a copy moves: 16 or 4 bytes where every tensor and every row of
   // channels is aligned to them, else single elements

@@ -486,6 +486,14 @@ def state_update_mimo(state, x, delta, A, B, C, D=None, y=None, stream=None):
 
 # --- gated recurrence and layer norm ------------------------------------------------
 
+def _current_stream_handle(index):
+    """The current stream's handle on device `index` (without the Stream
+    object that torch.cuda.current_stream makes, 3 us of a 10 us call)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(index).cuda_stream if raw is None else raw(index)
+
+
 def _on_stream(x, stream, inputs, call):
     """call(handle) -> tensors it allocated, made with x's device current and
     on `stream` (None: that device's current stream).  On another stream than
@@ -493,7 +501,7 @@ def _on_stream(x, stream, inputs, call):
     import torch
     device = x.device
     if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+        return call(_current_stream_handle(device.index))
     with torch.cuda.device(device):
         caller = torch.cuda.current_stream()
         if stream is None:
@@ -564,7 +572,7 @@ def gated_scan(x, gate, initial_state=None, return_final_state=True, gate_form="
         out = torch.empty_like(x) if y is None else y
         last = final_state
         if last is None and return_final_state:
-            last = torch.empty(rows, device=device, dtype=f32)
+            last = x.new_empty(rows, dtype=f32)
         mamba_gated_scan(x, gate, initial_state, out, last, checkpoints, batch, length, channels, flags, code, handle)
         return out, last
     return _on_stream(x, stream, (x, gate, initial_state, checkpoints), call)
@@ -603,7 +611,7 @@ def gated_scan_backward(x, gate, dy, initial_state=None, d_final_state=None, che
 
     def call(handle):
         dx, dgate = torch.empty_like(x), torch.empty_like(gate)
-        dh = torch.empty(rows, device=device, dtype=f32)
+        dh = x.new_empty(rows, dtype=f32)
         mamba_gated_scan_backward(x, gate, initial_state, checkpoints, dy, d_final_state, dx, dgate, dh, batch,
                                   length, channels, flags, code, handle)
         return dx, dgate, dh
@@ -659,8 +667,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, y=None, stream=No
 
     def call(handle):
         out = torch.empty_like(x) if y is None else y
-        mean = torch.empty(x.shape[:-1], device=device, dtype=f32)
-        rstd = torch.empty(x.shape[:-1], device=device, dtype=f32)
+        mean = x.new_empty(x.shape[:-1], dtype=f32)
+        rstd = torch.empty_like(mean)
         mamba_layer_norm(x, weight, bias, out, mean, rstd, rows, channels, eps, MAMBA_NORM_RMS if rms else 0, code,
                          handle)
         return out, mean, rstd
@@ -685,8 +693,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, rms=False, stream=
 
     def call(handle):
         dx = torch.empty_like(x)
-        dw = None if weight is None else torch.empty((channels,), device=device, dtype=f32)
-        db = torch.empty((channels,), device=device, dtype=f32) if bias else None
+        dw = None if weight is None else torch.empty_like(weight)
+        db = x.new_empty((channels,), dtype=f32) if bias else None
         mamba_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db, rows, channels,
                                   MAMBA_NORM_RMS if rms else 0, code, handle)
         return dx, dw, db
