@@ -44,16 +44,16 @@
 namespace mamba {
 
 constexpr int kGatedBlock = MAMBA_GATED_SCAN_BLOCK;  // tokens of a tile
-constexpr int kGatedThreads = 256;
+constexpr int kGatedWorkers = 256;                   // threads that hold tokens
+constexpr int kGatedThreads = kGatedWorkers + 32;    // and the control warp
 constexpr int kGatedSegs = 16;                       // segments of a tile
 constexpr int kGatedTok = kGatedBlock / kGatedSegs;  // tokens of a segment
 constexpr int kGatedRow = 64;                        // bytes of a token's channels in a tile
-// Two segments share a warp; 64 bytes between segments put them in different
-// halves of the banks.
-constexpr int kGatedSegBytes = kGatedTok * kGatedRow + 64;
+constexpr int kGatedSegBytes = kGatedTok * kGatedRow;
+constexpr int kGatedBox = 64;                        // tokens of a TMA box
 constexpr int kGatedStream = kGatedSegs * kGatedSegBytes;  // bytes of one tensor's tile
 constexpr int kGatedWindow = 8;                      // records looked at together
-static_assert(kGatedThreads == kGatedSegs * 16, "16 lanes per segment");
+static_assert(kGatedWorkers == kGatedSegs * 16, "16 lanes per segment");
 
 struct GatedArgs {
   const void* x;
@@ -83,14 +83,14 @@ struct GatedArgs {
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-__device__ __forceinline__ float2 rcp_newton(float2 d) {
+__device__ __forceinline__ float2 rcp_newton(float2 d, float2 minus_d) {
   // hardware reciprocal (1 ulp) and one Newton step: within 2^-24 of 1/d.  The
   // step is taken for bf16 data too: a state remembers thousands of gates, and
   // an error of one sign in each adds up in the float32 states.
   float2 r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
-  return __ffma2_rn(r, __ffma2_rn(make_float2(-d.x, -d.y), r, both(1.0f)), r);
+  return __ffma2_rn(r, __ffma2_rn(minus_d, r, both(1.0f)), r);
 }
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
@@ -131,7 +131,7 @@ template <bool LOG, bool FAST>
 __device__ __forceinline__ void gate_decay(float2 g, float2& a, float2& one_less) {
   if constexpr (!LOG) {
     const float2 e = gate_exp_neg<FAST>(g);
-    const float2 r = rcp_newton(__fadd2_rn(e, both(1.0f)));
+    const float2 r = rcp_newton(__fadd2_rn(e, both(1.0f)), __ffma2_rn(e, both(-1.0f), both(-1.0f)));
     one_less = __fmul2_rn(e, r);
     a = __fadd2_rn(r, both(-kGateTopRcp));
   } else if constexpr (FAST) {
@@ -196,14 +196,13 @@ struct Lane4 {
 };
 
 // ---------------------------------------------------------------------------
-// tile loads and stores.  CB: bytes a copy moves, 16, 4, or 2 (plain loads),
-// by the alignment of the tensors and of a row of channels.
+// tile loads and stores.  CB: what a load moves, by the alignment of the
+// tensors and of a row of channels: 16, a TMA box of a segment; 4, cp.async of
+// 4 bytes; 2, plain loads of single elements.
 // ---------------------------------------------------------------------------
 template <int CB>
 __device__ __forceinline__ void gated_copy(uint32_t dst, const unsigned char* src) {
-  if constexpr (CB == 16) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  } else if constexpr (CB == 4) {
+  if constexpr (CB == 4) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
   } else {
     const unsigned short v = *reinterpret_cast<const unsigned short*>(src);
@@ -211,32 +210,20 @@ __device__ __forceinline__ void gated_copy(uint32_t dst, const unsigned char* sr
   }
 }
 
-// rows [0, n) x bytes [0, width) of a tile whose first byte is src
+// rows [0, n) x bytes [0, width) of a tile whose first byte is src, by the workers
 template <int CB>
 __device__ __forceinline__ void gated_load(uint32_t dst, const unsigned char* src, int64_t pitch, int n, int width) {
   constexpr int kPer = kGatedRow / CB;         // copies per row
-  constexpr int kRows = kGatedThreads / kPer;  // rows per round
+  constexpr int kRows = kGatedWorkers / kPer;  // rows per round
+  static_assert(kGatedTok % kRows == 0, "whole rounds in a segment");
   const int col = ((int)threadIdx.x % kPer) * CB, r0 = (int)threadIdx.x / kPer;
   if (col >= width) return;
   src += r0 * pitch + col;
-  dst += (r0 / kGatedTok) * kGatedSegBytes + (r0 % kGatedTok) * kGatedRow + col;
-  auto at = [&](int i) {  // of row r0 + i kRows
-    if constexpr (kRows >= kGatedTok) return dst + i * (kRows / kGatedTok) * kGatedSegBytes;
-    else return dst + (i / (kGatedTok / kRows)) * kGatedSegBytes + (i % (kGatedTok / kRows)) * kRows * kGatedRow;
-  };
-  static_assert(kRows >= kGatedTok ? kRows % kGatedTok == 0 : kGatedTok % kRows == 0, "whole segments");
-  if (n == kGatedBlock) {
-#pragma unroll(CB == 16 ? 4 : 8)
-    for (int i = 0; i < kGatedBlock / kRows; ++i) {
-      gated_copy<CB>(at(i), src);
-      src += kRows * pitch;
-    }
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < kGatedBlock / kRows && r0 + i * kRows < n; ++i) {
-      gated_copy<CB>(at(i), src);
-      src += kRows * pitch;
-    }
+  dst += r0 * kGatedRow + col;
+#pragma unroll 8
+  for (int r = r0; r < n; r += kRows) {
+    gated_copy<CB>(dst + (r / kGatedTok) * kGatedSegBytes + (r % kGatedTok - r0) * kGatedRow, src);
+    src += kRows * pitch;
   }
 }
 
@@ -271,45 +258,33 @@ __device__ __forceinline__ unsigned long long rec_get(const unsigned long long* 
   return v;
 }
 
-// The state that enters the tile of `own`: from the nearest of the `before`
-// tiles before it whose record has P = 0, through the maps in between.
-// Records lie `stride` apart.  Called by a whole warp, a lane per channel.
-__device__ __forceinline__ float gated_look_back(const unsigned long long* own, int before, int64_t stride,
-                                                 bool active, uint64_t limit_ns) {
-  float h = 0.0f;
-  bool done = !active;
-  uint64_t t0 = 0;
-  for (uint32_t round = 0;; ++round) {
-    if (!done) {
-      unsigned long long r[kGatedWindow];
+// One look at the records before `own`: where the nearest of the `before` tiles
+// before it whose record has P = 0 is found, h is what enters, from there
+// through the maps in between.  Records lie `stride` apart.  For a whole warp,
+// a lane per channel; true once every lane is done.
+__device__ __forceinline__ bool gated_look_back(const unsigned long long* own, int before, int64_t stride, bool& done,
+                                                float& h) {
+  if (!done) {
+    unsigned long long r[kGatedWindow];
 #pragma unroll
-      for (int i = 0; i < kGatedWindow; ++i) r[i] = i < before ? rec_get(own - (i + 1) * stride) : 0ull;
-      int found = -1;
-      bool ready = true;
+    for (int i = 0; i < kGatedWindow; ++i) r[i] = i < before ? rec_get(own - (i + 1) * stride) : 0ull;
+    int found = -1;
+    bool ready = true;
 #pragma unroll
-      for (int i = 0; i < kGatedWindow; ++i) {
-        const uint32_t pb = (uint32_t)(r[i] >> 32);
-        ready = ready && pb != 0xffffffffu && i < before;
-        if (ready && found < 0 && __uint_as_float(pb) == 0.0f) found = i;
-      }
-      if (found >= 0) {
-        done = true;
-#pragma unroll
-        for (int i = kGatedWindow - 1; i >= 0; --i)
-          if (i <= found) h = fmaf(__uint_as_float((uint32_t)(r[i] >> 32)), h, __uint_as_float((uint32_t)r[i]));
-      }
+    for (int i = 0; i < kGatedWindow; ++i) {
+      const uint32_t pb = (uint32_t)(r[i] >> 32);
+      ready = ready && pb != 0xffffffffu && i < before;
+      if (ready && found < 0 && __uint_as_float(pb) == 0.0f) found = i;
     }
-    if (__all_sync(0xffffffffu, done)) return h;
-    if ((round & 63u) == 63u) {
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > limit_ns) {
-        record_device_error(MAMBA_ERR_TIMEOUT);
-        return h;
-      }
+    if (found >= 0) {
+      done = true;
+      h = 0.0f;
+#pragma unroll
+      for (int i = kGatedWindow - 1; i >= 0; --i)
+        if (i <= found) h = fmaf(__uint_as_float((uint32_t)(r[i] >> 32)), h, __uint_as_float((uint32_t)r[i]));
     }
   }
+  return __all_sync(0xffffffffu, done);
 }
 
 // Tile of a launch: chain (batch row, channel group) and time block.
@@ -320,6 +295,7 @@ struct __align__(16) GatedTile {
   int chain, b;  // chain, batch row
   int c0;        // first channel
   int n;         // tokens
+  int row;       // its first token's row of the [batch * len] rows
 };
 __device__ __forceinline__ int gated_div(int n, int d, unsigned rcp) {
   int q = (int)__umulhi((unsigned)n, rcp);  // at most one too small
@@ -338,36 +314,62 @@ __device__ __forceinline__ void gated_tile(const GatedArgs& p, int job, GatedTil
     const int block = REVERSE ? p.blocks - 1 - t.k : t.k;
     const int64_t t0 = (int64_t)block * kGatedBlock;
     t.n = (int)min((int64_t)kGatedBlock, p.len - t0);
-    t.at = ((int64_t)t.b * p.len + t0) * p.channels + t.c0;
+    t.row = (int)((int64_t)t.b * p.len + t0);
+    t.at = (int64_t)t.row * p.channels + t.c0;
   }
   *to = t;
 }
 
 constexpr int kGatedStages = 2;
 
-// Shared memory: the stages, the segments' maps (one float per segment and
-// channel each), what enters the tile, the stages' tiles.
+// Shared memory: the stages; the segments' maps (one float per segment and
+// channel each), forward for every other tile; what enters, for every other
+// tile; the tiles; barriers.
 template <typename TIO, bool BACKWARD>
 struct GatedSmem {
   static constexpr int kChan = kGatedRow / (int)sizeof(TIO);
-  static constexpr int kStage = (BACKWARD ? 3 : 2) * kGatedStream;
-  static constexpr int kMap = kGatedSegs * kChan * 4;
+  static constexpr int kStreams = BACKWARD ? 3 : 2;
+  static constexpr int kStage = kStreams * kGatedStream;
+  static constexpr int kPlane = kGatedSegs * kChan;        // floats
+  static constexpr int kMapSet = kStreams * kPlane;        // P, H and, backward, R
   static constexpr int kMaps = kGatedStages * kStage;
-  static constexpr int kEnter = kMaps + (BACKWARD ? 3 : 2) * kMap;
-  static constexpr int kTiles = kEnter + 2 * kChan * 4;
-  static constexpr int kFlag = kTiles + kGatedStages * (int)sizeof(GatedTile);
-  static constexpr int kBytes = kFlag + 16;
+  static constexpr int kMapSets = BACKWARD ? 1 : 2;  // two CTAs' backward stages leave room for one
+  static constexpr int kEnter = kMaps + kMapSets * kMapSet * 4;  // [2][what enters; backward: adjoint, state]
+  static constexpr int kTiles = kEnter + 2 * 2 * kChan * 4;
+  static constexpr int kBars = kTiles + 4 * (int)sizeof(GatedTile);
+  static constexpr int kBytes = kBars + 16 * 8;
 };
 
-// Tiles of a CTA: one per stage and one more held, each taken by itself, so
-// that the first ones of all CTAs come before anyone's second (a tile's map is
-// published only once the CTA's earlier tiles are done).  With one tile per CTA
-// at most, each takes just one.  One tile per chain: no order is needed, and
-// tiles are dealt by block index.
+// Barriers between the workers and the control warp.  full: a stage is loaded;
+// mapped: every warp's maps are written (and, forward, its stage is read);
+// entered: what enters the tile is written; state: backward, the state that
+// enters it; freed: backward, the stage is read to the end.
+struct GatedBars {
+  uint64_t full[kGatedStages], mapped[2], entered[2], state[2], freed[2];
+};
+
+// The next tile of a CTA, each taken by itself, so that the first ones of all
+// CTAs come before anyone's second (a tile's map is published only once the
+// CTA's earlier tiles are done).  With one tile per CTA at most, each takes just
+// one.  One tile per chain: no order is needed, and tiles are dealt by block
+// index.
 __device__ __forceinline__ int gated_next(const GatedArgs& p, int job) {
-  if (job >= 0 && p.jobs <= (int)gridDim.x) return p.jobs;
+  if (job >= 0 && (job >= p.jobs || p.jobs <= (int)gridDim.x)) return p.jobs;
   if (p.ticket) return atomicAdd(p.ticket, 1) + 1;
   return job < 0 ? (int)blockIdx.x : min(job + (int)gridDim.x, p.jobs);
+}
+
+// Waits end: everything waited for is bounded itself.  Once an error is on
+// record nobody waits long.
+__device__ __forceinline__ uint64_t gated_limit(const GatedArgs& p) {
+  return ld_volatile(&g_device_error) == 0 ? p.wait_limit_ns : 1000000ull;
+}
+__device__ __forceinline__ void gated_wait(const GatedArgs& p, uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return;
+  if (!mbar_wait_bounded(bar, parity, 2 * gated_limit(p))) record_device_error(MAMBA_ERR_TIMEOUT);
+}
+__device__ __forceinline__ void gated_arrive_async(uint64_t* bar) {  // when this thread's cp.async are done
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // The tile's map from its segments', in walking order
@@ -391,6 +393,12 @@ __device__ __forceinline__ float2 gated_pair(const float* p) {
   else return make_float2(*p, 0.0f);
 }
 
+template <int V>
+__device__ __forceinline__ void gated_put(float* p, float2 v) {
+  if constexpr (V == 2) *reinterpret_cast<float2*>(p) = v;
+  else *p = v.x;
+}
+
 // What enters this lane's segment: through the `count` segments before it in
 // walking order, from `h`, what enters the tile
 template <int V, int CHAN, bool REVERSE>
@@ -411,82 +419,232 @@ __device__ __forceinline__ float2 gated_enter(const float* seg_p, const float* s
   return h;
 }
 
-// One direction's carry, for warp 0 with a lane per channel.  peek: before the
-// tile's map is known, what entered if that is known already; publish: the
-// map, and later what leaves the tile.
-struct GatedCarry {
-  unsigned long long* rec;
-  int64_t stride;
-  unsigned long long seen;
-  float value;
-  bool active;
-  __device__ __forceinline__ void peek(const GatedArgs& p, const GatedTile& t, int chan, const float* start) {
-    const int lane = threadIdx.x;
-    active = lane < chan && t.c0 + lane < p.channels;
-    stride = (int64_t)p.chains * chan;
-    rec = p.rec + (int64_t)t.k * stride + t.chain * chan + (active ? lane : 0);
-    value = 0.0f;
-    seen = 0ull;
-    if (active && t.k > 0) seen = rec_get(rec - stride);
-    if (active && t.k == 0 && start) value = start[(int64_t)t.b * p.channels + t.c0 + lane];
+// ---------------------------------------------------------------------------
+// control warp: takes tiles, loads them (TMA), and works out and hands on what
+// enters and leaves them, a lane per channel
+// ---------------------------------------------------------------------------
+template <typename TIO, bool BACKWARD, int CB>
+struct GatedControl {
+  using SM = GatedSmem<TIO, BACKWARD>;
+  static constexpr int kChan = SM::kChan;
+  const GatedArgs& p;
+  unsigned char* smem;
+  GatedBars* bars;
+  GatedTile* tiles;
+  const CUtensorMap *gate, *x, *dy;
+
+  __device__ __forceinline__ GatedTile place(int it, int job) {
+    GatedTile t;
+    gated_tile<TIO, BACKWARD>(p, job, &t);
+    if ((threadIdx.x & 31) == 0) tiles[it & 3] = t;
+    __syncwarp();
+    return t;
   }
-  // whether what enters is known in every lane
-  __device__ __forceinline__ bool known(const GatedTile& t) {
-    const uint32_t pb = (uint32_t)(seen >> 32);
-    if (t.k > 0) value = __uint_as_float((uint32_t)seen);
-    return __all_sync(0xffffffffu, !active || pb == 0u || pb == 0x80000000u);
+  // tile `it` into its stage
+  __device__ __forceinline__ void load(int it, const GatedTile& t) {
+    if constexpr (CB == 16) {
+      const int lane = threadIdx.x & 31, stage = it % kGatedStages;
+      const int boxes = t.job < p.jobs ? (t.n + kGatedBox - 1) / kGatedBox : 0;
+      if (lane == 0) mbar_arrive_expect_tx(&bars->full[stage], SM::kStreams * boxes * kGatedBox * kGatedRow);
+      __syncwarp();
+      // a lane per box; boxes past the tensor's end are filled with zeros
+      const int stream = lane / (kGatedBlock / kGatedBox), box = lane % (kGatedBlock / kGatedBox);
+      if (stream < SM::kStreams && box < boxes)
+        tma_load_2d(smem + stage * SM::kStage + stream * kGatedStream + box * kGatedBox * kGatedRow,
+                    stream == 0 ? gate : stream == 1 ? x : dy, &bars->full[stage], t.c0, t.row + box * kGatedBox);
+    }
+  }
+  __device__ __forceinline__ int next(int job) {
+    int j = 0;
+    if ((threadIdx.x & 31) == 0) j = gated_next(p, job);
+    return __shfl_sync(0xffffffffu, j, 0);
+  }
+  __device__ __forceinline__ void first() {
+    int job = -1;
+#pragma unroll
+    for (int s = 0; s < kGatedStages; ++s) load(s, place(s, job = next(job)));
+  }
+  __device__ __forceinline__ bool all_looked(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+  }
+
+  __device__ __forceinline__ void run() {
+    const int lane = threadIdx.x & 31, ch = lane < kChan ? lane : 0;
+    const int64_t stride = (int64_t)p.chains * kChan;
+    for (int it = 0;; ++it) {
+      const GatedTile t = tiles[it & 3];
+      if (t.job >= p.jobs) return;
+      const int par = it & 1;
+      const uint32_t phase = (it >> 1) & 1;
+      int job = 0;  // of tile it + 2; its latency is hidden by what follows
+      if (lane == 0) job = gated_next(p, tiles[(it + 1) & 3].job);
+      if (CB < 16) place(it + 2, __shfl_sync(0xffffffffu, job, 0));  // the workers load it once past `entered`
+      const bool active = lane < kChan && t.c0 + lane < p.channels;
+      const int64_t row = (int64_t)t.b * p.channels + t.c0 + lane;
+      float* in = reinterpret_cast<float*>(smem + SM::kEnter) + par * 2 * kChan;
+      if constexpr (BACKWARD) {
+        const int64_t at = ((int64_t)t.b * p.blocks + p.blocks - 1 - t.k) * p.channels + t.c0 + lane;
+        if (lane < kChan) in[kChan + lane] = active ? p.ckpt[at] : 0.0f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->state[par]);
+      }
+      // backward: tile it + 1 goes where tile it - 1 was, once that is read to
+      // the end (before this tile is mapped)
+      bool due = BACKWARD && CB == 16 && it > 0;
+      auto reload = [&] {
+        load(it + 1, tiles[(it + 1) & 3]);
+        due = false;
+      };
+      const uint32_t phase_before = ((it - 1) >> 1) & 1;
+
+      // look for what enters while the workers make the tile's map
+      unsigned long long* rec = p.rec + (int64_t)t.k * stride + t.chain * kChan + ch;
+      const float* start = BACKWARD ? p.dh : p.h0;
+      float h = t.k == 0 && active && start ? start[row] : 0.0f;
+      bool done = !active || t.k == 0;
+      bool known = gated_look_back(rec, t.k, stride, done, h);
+      bool mapped = false;
+      while (!known && !mapped) {  // ends: the workers wait for nothing but loads
+        if (due && all_looked(&bars->freed[par ^ 1], phase_before)) reload();
+        mapped = all_looked(&bars->mapped[par], phase);
+        if (!mapped) known = gated_look_back(rec, t.k, stride, done, h);
+      }
+      auto tell = [&] {
+        if (lane < kChan) in[lane] = h;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->entered[par]);
+      };
+      if (known) tell();
+      if (due) {
+        if (!mapped) gated_wait(p, &bars->freed[par ^ 1], phase_before);
+        reload();
+      }
+      if (!mapped) gated_wait(p, &bars->mapped[par], phase);
+      const float* maps = reinterpret_cast<const float*>(smem + SM::kMaps) + par % SM::kMapSets * SM::kMapSet;
+      float tp, th;
+      gated_fold<kChan, BACKWARD>(maps, maps + (BACKWARD ? 2 : 1) * SM::kPlane, ch, tp, th);
+      const bool more = active && t.k + 1 < p.blocks;
+      if (!known) {
+        if (more) rec_put(rec, tp, th);
+        uint64_t t0 = 0;
+        for (uint32_t round = 0; !gated_look_back(rec, t.k, stride, done, h); ++round) {
+          if ((round & 63u) == 63u) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (__any_sync(0xffffffffu, now - t0 > gated_limit(p))) {
+              record_device_error(MAMBA_ERR_TIMEOUT);
+              break;
+            }
+          }
+        }
+        tell();
+      }
+      // what leaves, rounded as a reader of (P, H) rounds it
+      const float after = fmaf(tp, h, th);
+      if (more) rec_put(rec, 0.0f, after);
+      if (active) {
+        if (!BACKWARD && p.ckpt) p.ckpt[((int64_t)t.b * p.blocks + t.k) * p.channels + t.c0 + lane] = h;
+        float* out = BACKWARD ? p.dh0 : p.final_state;
+        if (t.k + 1 == p.blocks && out) out[row] = after;
+      }
+      if (CB == 16) {
+        const GatedTile ahead = place(it + 2, __shfl_sync(0xffffffffu, job, 0));
+        if (!BACKWARD) load(it + 2, ahead);  // the stage is read: its tile is mapped
+      }
+    }
   }
 };
+
+// What both kernels' CTAs start with; true for the control warp, which is then done.
+template <typename TIO, bool BACKWARD, int CB, typename Load>
+__device__ __forceinline__ bool gated_begin(const GatedArgs& p, unsigned char* smem, const CUtensorMap* gate,
+                                            const CUtensorMap* x, const CUtensorMap* dy, Load&& load) {
+  using SM = GatedSmem<TIO, BACKWARD>;
+  GatedBars* bars = reinterpret_cast<GatedBars*>(smem + SM::kBars);
+  GatedTile* tiles = reinterpret_cast<GatedTile*>(smem + SM::kTiles);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->full[i], CB == 16 ? 1 : kGatedWorkers);
+      mbar_init(&bars->mapped[i], kGatedWorkers / 32);
+      mbar_init(&bars->entered[i], 1);
+      mbar_init(&bars->state[i], 1);
+      mbar_init(&bars->freed[i], kGatedWorkers / 32);
+    }
+    fence_mbar_init();
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+  __syncthreads();
+  const bool control = threadIdx.x >= kGatedWorkers;
+  GatedControl<TIO, BACKWARD, CB> c{p, smem, bars, tiles, gate, x, dy};
+  if (control) c.first();
+  if (CB < 16) {
+    __syncthreads();
+    if (!control) {
+#pragma unroll
+      for (int s = 0; s < kGatedStages; ++s) load(s);
+    }
+  }
+  if (control) c.run();
+  return control;
+}
+
+// A worker's part of loading tile `it` where there is no TMA
+template <typename TIO, bool BACKWARD, int CB>
+__device__ __forceinline__ void gated_worker_load(const GatedArgs& p, unsigned char* smem, int it) {
+  if constexpr (CB < 16) {
+    using SM = GatedSmem<TIO, BACKWARD>;
+    constexpr int kES = (int)sizeof(TIO);
+    const int stage = it % kGatedStages;
+    GatedBars* bars = reinterpret_cast<GatedBars*>(smem + SM::kBars);
+    const GatedTile& t = reinterpret_cast<const GatedTile*>(smem + SM::kTiles)[it & 3];
+    if (t.job < p.jobs) {
+      const int width = (int)min((int64_t)kGatedRow, (p.channels - t.c0) * kES);
+      const int64_t pitch = p.channels * kES;
+      const uint32_t to = smem_addr(smem) + stage * SM::kStage;
+      gated_load<CB>(to, static_cast<const unsigned char*>(p.gate) + t.at * kES, pitch, t.n, width);
+      gated_load<CB>(to + kGatedStream, static_cast<const unsigned char*>(p.x) + t.at * kES, pitch, t.n, width);
+      if (BACKWARD)
+        gated_load<CB>(to + 2 * kGatedStream, static_cast<const unsigned char*>(p.dy) + t.at * kES, pitch, t.n, width);
+    }
+    if (CB == 4) gated_arrive_async(&bars->full[stage]);
+    else mbar_arrive(&bars->full[stage]);
+  }
+}
+
+__device__ __forceinline__ void gated_warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 template <typename TIO, bool LOG, bool CONVEX, int CB>
-__global__ void __launch_bounds__(kGatedThreads, 2) gated_scan_kernel(const GatedArgs p) {
+__global__ void __launch_bounds__(kGatedThreads, 2)
+gated_scan_kernel(const GatedArgs p, const __grid_constant__ CUtensorMap map_gate,
+                  const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy) {
   using L4 = Lane4<TIO>;
   using SM = GatedSmem<TIO, false>;
   constexpr int V = L4::kV, W = L4::kWords, kChan = SM::kChan, kES = (int)sizeof(TIO), kPairs = kGatedTok / W;
-  extern __shared__ __align__(16) unsigned char smem[];
-  float* seg_p = reinterpret_cast<float*>(smem + SM::kMaps);  // [segment][channel]
-  float* seg_h = seg_p + kGatedSegs * kChan;
-  float* enter = reinterpret_cast<float*>(smem + SM::kEnter);
-  GatedTile* tiles = reinterpret_cast<GatedTile*>(smem + SM::kTiles);
-  int* flag = reinterpret_cast<int*>(smem + SM::kFlag);
+  extern __shared__ __align__(128) unsigned char gated_smem[];
+  unsigned char* smem = gated_smem;
+  auto load = [&](int it) { gated_worker_load<TIO, false, CB>(p, smem, it); };
+  if (gated_begin<TIO, false, CB>(p, smem, &map_gate, &map_x, &map_dy, load)) return;
+  GatedBars* bars = reinterpret_cast<GatedBars*>(smem + SM::kBars);
   const int tid = threadIdx.x, seg = tid >> 4, col = (tid & 15) * V;
-  const uint32_t stage0 = smem_addr(smem), mine = seg * kGatedSegBytes + (tid & 15) * 4;
+  const uint32_t mine = smem_addr(smem) + seg * kGatedSegBytes + (tid & 15) * 4;
   const int64_t pitch = p.channels * kES;
-  griddep_launch_dependents();
-  griddep_wait();
 
-  int held = -1;  // thread 32: the tile after those of the stages
-  auto load = [&](int stage) {
-    const GatedTile& t = tiles[stage];
-    if (t.job < p.jobs) {
-      const int width = (int)min((int64_t)kGatedRow, (p.channels - t.c0) * kES);
-      const uint32_t to = stage0 + stage * SM::kStage;
-      gated_load<CB>(to, static_cast<const unsigned char*>(p.gate) + t.at * kES, pitch, t.n, width);
-      gated_load<CB>(to + kGatedStream, static_cast<const unsigned char*>(p.x) + t.at * kES, pitch, t.n, width);
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < kGatedStages; ++s) {
-    if (tid == 32) gated_tile<TIO, false>(p, held = gated_next(p, held), tiles + s);
-    __syncthreads();
-    load(s);
-  }
-  if (tid == 32) held = gated_next(p, held);
-
-  for (int stage = 0;; stage = stage + 1 == kGatedStages ? 0 : stage + 1) {
-    const GatedTile t = tiles[stage];
-    if (t.job >= p.jobs) break;
-    cp_async_wait<kGatedStages - 1>();
-    __syncthreads();
-    GatedCarry carry;
-    if (tid < 32) carry.peek(p, t, kChan, p.h0);
+  for (int it = 0;; ++it) {
+    const int par = it & 1;
+    const uint32_t phase = (it >> 1) & 1;
+    gated_wait(p, &bars->full[par], phase);
+    const GatedTile t = reinterpret_cast<const GatedTile*>(smem + SM::kTiles)[it & 3];
+    if (t.job >= p.jobs) return;
 
     // the segment's gates and inputs, and its map
-    const uint32_t from = stage0 + stage * SM::kStage + mine;
+    const uint32_t from = mine + par * SM::kStage;
     const int n = t.n - seg * kGatedTok;
     float2 a[kPairs], b[kPairs], P = both(1.0f), H = both(0.0f);
     auto map = [&](auto full) {
@@ -512,47 +670,18 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_scan_kernel(const Gate
     };
     if (t.n == kGatedBlock) map(std::true_type{});
     else map(std::false_type{});
-    if constexpr (V == 2) {
-      *reinterpret_cast<float2*>(seg_p + seg * kChan + col) = P;
-      *reinterpret_cast<float2*>(seg_h + seg * kChan + col) = H;
-    } else {
-      seg_p[seg * kChan + col] = P.x;
-      seg_h[seg * kChan + col] = H.x;
-    }
-    if (tid < 32) {
-      const bool known = carry.known(t);
-      if (tid < kChan) enter[tid] = carry.value;
-      if (tid == 0) *flag = known;
-    } else if (tid == 32) {
-      gated_tile<TIO, false>(p, held, tiles + stage);
-      held = gated_next(p, held);
-    }
-    __syncthreads();
-    load(stage);
-
-    const bool known = *flag != 0;
-    if (tid < 32) {
-      const int ch = tid < kChan ? tid : 0;
-      float tp, th;
-      gated_fold<kChan, false>(seg_p, seg_h, ch, tp, th);
-      const bool more = carry.active && t.k + 1 < p.blocks;
-      if (!known) {
-        if (more) rec_put(carry.rec, tp, th);
-        carry.value = gated_look_back(carry.rec, t.k, carry.stride, carry.active, p.wait_limit_ns);
-        if (tid < kChan) enter[tid] = carry.value;
-      }
-      // what leaves, rounded as a reader of (P, H) rounds it
-      const float after = fmaf(tp, carry.value, th);
-      if (more) rec_put(carry.rec, 0.0f, after);
-      if (carry.active) {
-        if (p.ckpt) p.ckpt[((int64_t)t.b * p.blocks + t.k) * p.channels + t.c0 + ch] = carry.value;
-        if (t.k + 1 == p.blocks && p.final_state) p.final_state[(int64_t)t.b * p.channels + t.c0 + ch] = after;
-      }
-    }
-    if (!known) __syncthreads();
+    float* seg_p = reinterpret_cast<float*>(smem + SM::kMaps) + par * SM::kMapSet + col;  // [segment][channel]
+    float* seg_h = seg_p + SM::kPlane;
+    gated_put<V>(seg_p + seg * kChan, P);
+    gated_put<V>(seg_h + seg * kChan, H);
+    gated_warp_arrive(&bars->mapped[par]);
+    gated_wait(p, &bars->mapped[par], phase);
+    gated_wait(p, &bars->entered[par], phase);
+    load(it + kGatedStages);
 
     if (p.y && t.c0 + col < p.channels) {
-      float2 h = gated_enter<V, kChan, false>(seg_p + col, seg_h + col, seg, gated_pair<V>(enter + col));
+      const float* enter = reinterpret_cast<const float*>(smem + SM::kEnter) + par * 2 * kChan + col;
+      float2 h = gated_enter<V, kChan, false>(seg_p, seg_h, seg, gated_pair<V>(enter));
       unsigned char* y = static_cast<unsigned char*>(p.y) + (t.at + (int64_t)seg * kGatedTok * p.channels + col) * kES;
       const int left = (int)min((int64_t)4, (p.channels - t.c0 - col) * kES);
       auto out = [&](auto full) {
@@ -579,57 +708,30 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_scan_kernel(const Gate
 // The adjoint's map of a segment takes c = a_{t+1} lam_{t+1} of the token after
 // it to a_s lam_s of its first token s: c -> P c + R, R = sum of dy_t a_s..a_t.
 template <typename TIO, bool LOG, bool CONVEX, int CB>
-__global__ void __launch_bounds__(kGatedThreads, 2) gated_backward_kernel(const GatedArgs p) {
+__global__ void __launch_bounds__(kGatedThreads, 2)
+gated_backward_kernel(const GatedArgs p, const __grid_constant__ CUtensorMap map_gate,
+                      const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy) {
   using L4 = Lane4<TIO>;
   using SM = GatedSmem<TIO, true>;
   constexpr int V = L4::kV, W = L4::kWords, kChan = SM::kChan, kES = (int)sizeof(TIO), kPairs = kGatedTok / W;
   constexpr bool kFast = kES == 2;
-  extern __shared__ __align__(16) unsigned char smem[];
-  float* seg_p = reinterpret_cast<float*>(smem + SM::kMaps);  // [segment][channel]
-  float* seg_h = seg_p + kGatedSegs * kChan;
-  float* seg_r = seg_h + kGatedSegs * kChan;
-  float* enter = reinterpret_cast<float*>(smem + SM::kEnter);  // adjoint, from the right
-  float* enter_h = enter + kChan;                              // state, from the left
-  GatedTile* tiles = reinterpret_cast<GatedTile*>(smem + SM::kTiles);
-  int* flag = reinterpret_cast<int*>(smem + SM::kFlag);
+  extern __shared__ __align__(128) unsigned char gated_smem[];
+  unsigned char* smem = gated_smem;
+  auto load = [&](int it) { gated_worker_load<TIO, true, CB>(p, smem, it); };
+  if (gated_begin<TIO, true, CB>(p, smem, &map_gate, &map_x, &map_dy, load)) return;
+  GatedBars* bars = reinterpret_cast<GatedBars*>(smem + SM::kBars);
   const int tid = threadIdx.x, seg = tid >> 4, col = (tid & 15) * V;
-  const uint32_t stage0 = smem_addr(smem), mine = seg * kGatedSegBytes + (tid & 15) * 4;
+  const uint32_t mine = smem_addr(smem) + seg * kGatedSegBytes + (tid & 15) * 4;
   const int64_t pitch = p.channels * kES;
-  griddep_launch_dependents();
-  griddep_wait();
 
-  int held = -1;
-  auto load = [&](int stage) {
-    const GatedTile& t = tiles[stage];
-    if (t.job < p.jobs) {
-      const int width = (int)min((int64_t)kGatedRow, (p.channels - t.c0) * kES);
-      const uint32_t to = stage0 + stage * SM::kStage;
-      gated_load<CB>(to, static_cast<const unsigned char*>(p.gate) + t.at * kES, pitch, t.n, width);
-      gated_load<CB>(to + kGatedStream, static_cast<const unsigned char*>(p.x) + t.at * kES, pitch, t.n, width);
-      gated_load<CB>(to + 2 * kGatedStream, static_cast<const unsigned char*>(p.dy) + t.at * kES, pitch, t.n, width);
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < kGatedStages; ++s) {
-    if (tid == 32) gated_tile<TIO, true>(p, held = gated_next(p, held), tiles + s);
-    __syncthreads();
-    load(s);
-  }
-  if (tid == 32) held = gated_next(p, held);
+  for (int it = 0;; ++it) {
+    const int par = it & 1;
+    const uint32_t phase = (it >> 1) & 1;
+    gated_wait(p, &bars->full[par], phase);
+    const GatedTile t = reinterpret_cast<const GatedTile*>(smem + SM::kTiles)[it & 3];
+    if (t.job >= p.jobs) return;
 
-  for (int stage = 0;; stage = stage + 1 == kGatedStages ? 0 : stage + 1) {
-    const GatedTile t = tiles[stage];
-    if (t.job >= p.jobs) break;
-    cp_async_wait<kGatedStages - 1>();
-    __syncthreads();
-    GatedCarry carry;
-    float state = 0.0f;
-    if (tid < 32) carry.peek(p, t, kChan, p.dh);
-    if (tid >= 64 && tid < 64 + kChan && t.c0 + tid - 64 < p.channels)
-      state = p.ckpt[((int64_t)t.b * p.blocks + p.blocks - 1 - t.k) * p.channels + t.c0 + tid - 64];
-
-    const uint32_t from = stage0 + stage * SM::kStage + mine;
+    const uint32_t from = mine + par * SM::kStage;
     const int n = t.n - seg * kGatedTok;
     float2 a[kPairs], b[kPairs], P = both(1.0f), H = both(0.0f), R = both(0.0f);
     auto map = [&](auto full) {
@@ -663,46 +765,21 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_backward_kernel(const 
     };
     if (t.n == kGatedBlock) map(std::true_type{});
     else map(std::false_type{});
-    if constexpr (V == 2) {
-      *reinterpret_cast<float2*>(seg_p + seg * kChan + col) = P;
-      *reinterpret_cast<float2*>(seg_h + seg * kChan + col) = H;
-      *reinterpret_cast<float2*>(seg_r + seg * kChan + col) = R;
-    } else {
-      seg_p[seg * kChan + col] = P.x;
-      seg_h[seg * kChan + col] = H.x;
-      seg_r[seg * kChan + col] = R.x;
-    }
-    if (tid < 32) {
-      const bool known = carry.known(t);
-      if (tid < kChan) enter[tid] = carry.value;
-      if (tid == 0) *flag = known;
-    } else if (tid == 32) {
-      gated_tile<TIO, true>(p, held, tiles + stage);
-      held = gated_next(p, held);
-    }
-    if (tid >= 64 && tid < 64 + kChan) enter_h[tid - 64] = state;
-    __syncthreads();
-
-    const bool known = *flag != 0;
-    if (tid < 32) {
-      const int ch = tid < kChan ? tid : 0;
-      float tp, tr;
-      gated_fold<kChan, true>(seg_p, seg_r, ch, tp, tr);
-      const bool more = carry.active && t.k + 1 < p.blocks;
-      if (!known) {
-        if (more) rec_put(carry.rec, tp, tr);
-        carry.value = gated_look_back(carry.rec, t.k, carry.stride, carry.active, p.wait_limit_ns);
-        if (tid < kChan) enter[tid] = carry.value;
-      }
-      const float after = fmaf(tp, carry.value, tr);
-      if (more) rec_put(carry.rec, 0.0f, after);
-      if (carry.active && t.k + 1 == p.blocks && p.dh0) p.dh0[(int64_t)t.b * p.channels + t.c0 + ch] = after;
-    }
+    if (it > 0) gated_wait(p, &bars->freed[par ^ 1], ((it - 1) >> 1) & 1);  // the last tile's maps are read
+    float* seg_p = reinterpret_cast<float*>(smem + SM::kMaps) + col;  // [segment][channel]
+    float* seg_h = seg_p + SM::kPlane;
+    float* seg_r = seg_h + SM::kPlane;
+    gated_put<V>(seg_p + seg * kChan, P);
+    gated_put<V>(seg_h + seg * kChan, H);
+    gated_put<V>(seg_r + seg * kChan, R);
+    gated_warp_arrive(&bars->mapped[par]);
+    gated_wait(p, &bars->mapped[par], phase);
+    gated_wait(p, &bars->state[par], phase);
 
     // b becomes h_{t-1} (minus x_t when convex)
-    const bool mine_live = t.c0 + col < p.channels;
+    const float* enter = reinterpret_cast<const float*>(smem + SM::kEnter) + par * 2 * kChan + col;
     {
-      float2 h = gated_enter<V, kChan, false>(seg_p + col, seg_h + col, seg, gated_pair<V>(enter_h + col));
+      float2 h = gated_enter<V, kChan, false>(seg_p, seg_h, seg, gated_pair<V>(enter + kChan));
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         float2 before, after;
@@ -711,17 +788,16 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_backward_kernel(const 
           uint32_t xw[W];
 #pragma unroll
           for (int k = 0; k < W; ++k) xw[k] = lds32(from + kGatedStream + (i * W + k) * kGatedRow);
-          const float2 x = L4::get(xw);
-          b[i] = __fadd2_rn(before, make_float2(-x.x, -x.y));
+          b[i] = __ffma2_rn(L4::get(xw), both(-1.0f), before);
         } else {
           b[i] = before;
         }
       }
     }
-    if (!known) __syncthreads();
+    gated_wait(p, &bars->entered[par], phase);
 
-    if (mine_live) {
-      float2 c = gated_enter<V, kChan, true>(seg_p + col, seg_r + col, kGatedSegs - 1 - seg, gated_pair<V>(enter + col));
+    if (t.c0 + col < p.channels) {
+      float2 c = gated_enter<V, kChan, true>(seg_p, seg_r, kGatedSegs - 1 - seg, gated_pair<V>(enter));
       const int64_t at = (t.at + (int64_t)seg * kGatedTok * p.channels + col) * kES;
       unsigned char* dx = static_cast<unsigned char*>(p.dx) + at;
       unsigned char* dg = static_cast<unsigned char*>(p.dgate) + at;
@@ -768,8 +844,11 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_backward_kernel(const 
       if (t.n == kGatedBlock) out(std::true_type{});
       else out(std::false_type{});
     }
-    __syncthreads();  // the stage is read to the end
-    load(stage);
+    gated_warp_arrive(&bars->freed[par]);  // the stage is read to the end
+    if (CB < 16) {
+      gated_wait(p, &bars->freed[par], phase);
+      load(it + kGatedStages);
+    }
   }
 }
 

@@ -869,10 +869,9 @@ int launch_1d(void (*kernel)(K...), int64_t blocks, int threads, cudaStream_t st
   return cudaGetLastError() == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA;
 }
 
-// One pass over every tile: the forward kernel, or the backward one.  rec and
-// ticket are scratch of gated_scratch_bytes for this pass, or NULL.
+// One pass over every tile: the forward kernel, or the backward one
 template <typename TIO, bool LOG, bool CONVEX, bool BACKWARD, int CB>
-int launch_gated_pass(const GatedArgs& p, cudaStream_t stream) {
+int launch_gated_pass(const GatedArgs& p, const CUtensorMap (&maps)[3], cudaStream_t stream) {
   int sms = 0;
   if (int st = current_sms(&sms)) return st;
   constexpr int kBytes = GatedSmem<TIO, BACKWARD>::kBytes;
@@ -883,8 +882,10 @@ int launch_gated_pass(const GatedArgs& p, cudaStream_t stream) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
     return MAMBA_ERR_CUDA;
   const unsigned ctas = (unsigned)std::min<int64_t>(p.jobs, 2 * (int64_t)sms);
-  return launch_pdl(kernel, dim3(ctas), dim3(kGatedThreads), (size_t)kBytes, stream, p) == cudaSuccess ? MAMBA_OK
-                                                                                                    : MAMBA_ERR_CUDA;
+  return launch_pdl(kernel, dim3(ctas), dim3(kGatedThreads), (size_t)kBytes, stream, p, maps[0], maps[1], maps[2]) ==
+                 cudaSuccess
+             ? MAMBA_OK
+             : MAMBA_ERR_CUDA;
 }
 
 int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int dtype, cudaStream_t stream) {
@@ -905,7 +906,16 @@ int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int 
     return (p.channels * es) % (int64_t)a == 0 && aligned(p.x, a) && aligned(p.gate, a) && aligned(p.dy, a) &&
            aligned(p.y, a) && aligned(p.dx, a) && aligned(p.dgate, a);
   };
-  const int cb = all_aligned(16) ? 16 : all_aligned(4) ? 4 : 2;
+  int cb = all_aligned(16) ? 16 : all_aligned(4) ? 4 : 2;
+  CUtensorMap maps[3];
+  std::memset(maps, 0, sizeof(maps));
+  if (cb == 16) {
+    const void* from[3] = {p.gate, p.x, p.dy};
+    for (int i = 0; i < (backward ? 3 : 2); ++i)
+      if (!make_map_2d(&maps[i], from[i], dtype, (uint64_t)p.channels, (uint64_t)(batch * p.len), (uint32_t)chan,
+                       kGatedBox))
+        cb = 4;
+  }
   // scratch: records and a counter for every pass over several tiles of time,
   // and the checkpoints that a backward call has not been given
   const bool own_ckpt = backward && !p.ckpt;
@@ -933,16 +943,16 @@ int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int 
       if constexpr (CB == 2 && sizeof(TIO) == 4) {
         return MAMBA_ERR_INVALID_ARG;  // float32 tensors are 4-byte aligned
       } else {
-        if (!backward) return launch_gated_pass<TIO, L, C, false, CB>(scratch_of(p, 0), stream);
+        if (!backward) return launch_gated_pass<TIO, L, C, false, CB>(scratch_of(p, 0), maps, stream);
         int e = MAMBA_OK;
         GatedArgs q = scratch_of(p, 0);
         if (own_ckpt) {
           q.ckpt = reinterpret_cast<float*>(mem + passes);
           GatedArgs f = scratch_of(q, 1);
           f.y = nullptr;
-          e = launch_gated_pass<TIO, L, C, false, CB>(f, stream);
+          e = launch_gated_pass<TIO, L, C, false, CB>(f, maps, stream);
         }
-        return e == MAMBA_OK ? launch_gated_pass<TIO, L, C, true, CB>(q, stream) : e;
+        return e == MAMBA_OK ? launch_gated_pass<TIO, L, C, true, CB>(q, maps, stream) : e;
       }
     });
   };
