@@ -45,12 +45,11 @@ namespace mamba {
 
 constexpr int kGatedBlock = MAMBA_GATED_SCAN_BLOCK;  // tokens of a tile
 constexpr int kGatedWorkers = 256;                   // threads that hold tokens
-constexpr int kGatedThreads = kGatedWorkers + 32;    // and the control warp
+constexpr int kGatedThreads = kGatedWorkers + 64;    // and the carrier's and the loader's warp
 constexpr int kGatedSegs = 16;                       // segments of a tile
 constexpr int kGatedTok = kGatedBlock / kGatedSegs;  // tokens of a segment
 constexpr int kGatedRow = 64;                        // bytes of a token's channels in a tile
 constexpr int kGatedSegBytes = kGatedTok * kGatedRow;
-constexpr int kGatedBox = 64;                        // tokens of a TMA box
 constexpr int kGatedStream = kGatedSegs * kGatedSegBytes;  // bytes of one tensor's tile
 constexpr int kGatedWindow = 8;                      // records looked at together
 static_assert(kGatedWorkers == kGatedSegs * 16, "16 lanes per segment");
@@ -68,13 +67,13 @@ struct GatedArgs {
   void* dgate;
   float* dh0;
   unsigned long long* rec;  // [blocks][chains][channels of a tile] records, all bits set
-  int* ticket;           // tiles handed out, starting at -1; NULL: one tile per chain, dealt by block index
   int64_t len, channels;
   int blocks;            // tiles along time
   int groups;            // channel groups
   int chains;            // batch * groups
   int jobs;              // chains * blocks
   unsigned rcp_chains, rcp_groups;  // floor(2^32 / ...), for divisions
+  int box;               // tokens of a TMA box
   uint64_t wait_limit_ns;
 };
 
@@ -258,34 +257,39 @@ __device__ __forceinline__ unsigned long long rec_get(const unsigned long long* 
   return v;
 }
 
-// One look at the records before `own`: where the nearest of the `before` tiles
+// A look at the records before `own`: where the nearest of the `before` tiles
 // before it whose record has P = 0 is found, h is what enters, from there
 // through the maps in between.  Records lie `stride` apart.  For a whole warp,
-// a lane per channel; true once every lane is done.
-__device__ __forceinline__ bool gated_look_back(const unsigned long long* own, int before, int64_t stride, bool& done,
-                                                float& h) {
-  if (!done) {
-    unsigned long long r[kGatedWindow];
+// a lane per channel: ask() sends for the records, found() is true once every
+// lane is done.
+struct GatedLook {
+  unsigned long long r[kGatedWindow];
+  __device__ __forceinline__ void ask(const unsigned long long* own, int before, int64_t stride, bool done) {
 #pragma unroll
-    for (int i = 0; i < kGatedWindow; ++i) r[i] = i < before ? rec_get(own - (i + 1) * stride) : 0ull;
-    int found = -1;
-    bool ready = true;
+    for (int i = 0; i < kGatedWindow; ++i) {
+      r[i] = ~0ull;
+      if (!done && i < before) r[i] = rec_get(own - (i + 1) * stride);
+    }
+  }
+  __device__ __forceinline__ bool found(bool& done, float& h) {
+    int at = -1;
+    bool ready = !done;
 #pragma unroll
     for (int i = 0; i < kGatedWindow; ++i) {
       const uint32_t pb = (uint32_t)(r[i] >> 32);
-      ready = ready && pb != 0xffffffffu && i < before;
-      if (ready && found < 0 && __uint_as_float(pb) == 0.0f) found = i;
+      ready = ready && pb != 0xffffffffu;
+      if (ready && at < 0 && __uint_as_float(pb) == 0.0f) at = i;
     }
-    if (found >= 0) {
+    if (at >= 0) {
       done = true;
       h = 0.0f;
 #pragma unroll
       for (int i = kGatedWindow - 1; i >= 0; --i)
-        if (i <= found) h = fmaf(__uint_as_float((uint32_t)(r[i] >> 32)), h, __uint_as_float((uint32_t)r[i]));
+        if (i <= at) h = fmaf(__uint_as_float((uint32_t)(r[i] >> 32)), h, __uint_as_float((uint32_t)r[i]));
     }
+    return __all_sync(0xffffffffu, done);
   }
-  return __all_sync(0xffffffffu, done);
-}
+};
 
 // Tile of a launch: chain (batch row, channel group) and time block.
 struct __align__(16) GatedTile {
@@ -340,24 +344,15 @@ struct GatedSmem {
   static constexpr int kBytes = kBars + 16 * 8;
 };
 
-// Barriers between the workers and the control warp.  full: a stage is loaded;
-// mapped: every warp's maps are written (and, forward, its stage is read);
-// entered: what enters the tile is written; state: backward, the state that
-// enters it; freed: backward, the stage is read to the end.
+// Barriers between the workers (w), the carrier (c) and the loader (l).  full,
+// l to w and c: a stage is loaded (backward, with the states that enter);
+// mapped, w to c and l: every warp's maps are written (and, forward, its stage
+// is read); entered, c to w: what enters the tile is written; freed, w to w and
+// l: backward, the stage is read to the end; placed, l to w: without TMA, the
+// tile that the workers are to load is known.
 struct GatedBars {
-  uint64_t full[kGatedStages], mapped[2], entered[2], state[2], freed[2];
+  uint64_t full[kGatedStages], mapped[2], entered[2], freed[2], placed[2];
 };
-
-// The next tile of a CTA, each taken by itself, so that the first ones of all
-// CTAs come before anyone's second (a tile's map is published only once the
-// CTA's earlier tiles are done).  With one tile per CTA at most, each takes just
-// one.  One tile per chain: no order is needed, and tiles are dealt by block
-// index.
-__device__ __forceinline__ int gated_next(const GatedArgs& p, int job) {
-  if (job >= 0 && (job >= p.jobs || p.jobs <= (int)gridDim.x)) return p.jobs;
-  if (p.ticket) return atomicAdd(p.ticket, 1) + 1;
-  return job < 0 ? (int)blockIdx.x : min(job + (int)gridDim.x, p.jobs);
-}
 
 // Waits end: everything waited for is bounded itself.  Once an error is on
 // record nobody waits long.
@@ -420,173 +415,134 @@ __device__ __forceinline__ float2 gated_enter(const float* seg_p, const float* s
 }
 
 // ---------------------------------------------------------------------------
-// control warp: takes tiles, loads them (TMA), and works out and hands on what
-// enters and leaves them, a lane per channel
+// loader warp: takes tiles and loads them
 // ---------------------------------------------------------------------------
 template <typename TIO, bool BACKWARD, int CB>
-struct GatedControl {
+struct GatedLoader {
   using SM = GatedSmem<TIO, BACKWARD>;
-  static constexpr int kChan = SM::kChan;
   const GatedArgs& p;
   unsigned char* smem;
   GatedBars* bars;
-  GatedTile* tiles;
   const CUtensorMap *gate, *x, *dy;
 
   __device__ __forceinline__ GatedTile place(int it, int job) {
     GatedTile t;
     gated_tile<TIO, BACKWARD>(p, job, &t);
-    if ((threadIdx.x & 31) == 0) tiles[it & 3] = t;
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<GatedTile*>(smem + SM::kTiles)[it & 3] = t;
     __syncwarp();
     return t;
   }
-  // tile `it` into its stage
+  // tile `it` into its stage; boxes past the tensor's end are filled with zeros
   __device__ __forceinline__ void load(int it, const GatedTile& t) {
-    if constexpr (CB == 16) {
-      const int lane = threadIdx.x & 31, stage = it % kGatedStages;
-      const int boxes = t.job < p.jobs ? (t.n + kGatedBox - 1) / kGatedBox : 0;
-      if (lane == 0) mbar_arrive_expect_tx(&bars->full[stage], SM::kStreams * boxes * kGatedBox * kGatedRow);
+    const int lane = threadIdx.x & 31, stage = it % kGatedStages;
+    if (CB == 16 && lane == 0) {
+      const int rows = t.job < p.jobs ? (t.n + p.box - 1) / p.box * p.box : 0;
+      mbar_arrive_expect_tx(&bars->full[stage], SM::kStreams * rows * kGatedRow);
+      unsigned char* to = smem + stage * SM::kStage;
+      for (int r = 0; r < rows; r += p.box) {
+        tma_load_2d(to + r * kGatedRow, gate, &bars->full[stage], t.c0, t.row + r);
+        tma_load_2d(to + kGatedStream + r * kGatedRow, x, &bars->full[stage], t.c0, t.row + r);
+        if (BACKWARD) tma_load_2d(to + 2 * kGatedStream + r * kGatedRow, dy, &bars->full[stage], t.c0, t.row + r);
+      }
+    }
+    if (BACKWARD) {  // the states that enter
+      const int64_t at = ((int64_t)t.b * p.blocks + p.blocks - 1 - t.k) * p.channels + t.c0 + lane;
+      const bool active = t.job < p.jobs && lane < SM::kChan && t.c0 + lane < p.channels;
+      float* in = reinterpret_cast<float*>(smem + SM::kEnter) + stage * 2 * SM::kChan + SM::kChan;
+      const float h = active ? p.ckpt[at] : 0.0f;
+      if (lane < SM::kChan) in[lane] = h;
       __syncwarp();
-      // a lane per box; boxes past the tensor's end are filled with zeros
-      const int stream = lane / (kGatedBlock / kGatedBox), box = lane % (kGatedBlock / kGatedBox);
-      if (stream < SM::kStreams && box < boxes)
-        tma_load_2d(smem + stage * SM::kStage + stream * kGatedStream + box * kGatedBox * kGatedRow,
-                    stream == 0 ? gate : stream == 1 ? x : dy, &bars->full[stage], t.c0, t.row + box * kGatedBox);
+      if (lane == 0) mbar_arrive(&bars->full[stage]);
     }
   }
-  __device__ __forceinline__ int next(int job) {
-    int j = 0;
-    if ((threadIdx.x & 31) == 0) j = gated_next(p, job);
-    return __shfl_sync(0xffffffffu, j, 0);
-  }
-  __device__ __forceinline__ void first() {
-    int job = -1;
-#pragma unroll
-    for (int s = 0; s < kGatedStages; ++s) load(s, place(s, job = next(job)));
-  }
-  __device__ __forceinline__ bool all_looked(uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
-  }
-
   __device__ __forceinline__ void run() {
-    const int lane = threadIdx.x & 31, ch = lane < kChan ? lane : 0;
-    const int64_t stride = (int64_t)p.chains * kChan;
-    for (int it = 0;; ++it) {
-      const GatedTile t = tiles[it & 3];
-      if (t.job >= p.jobs) return;
+    int job = blockIdx.x;
+#pragma unroll
+    for (int s = 0; s < kGatedStages; ++s, job = min(job + (int)gridDim.x, p.jobs)) {
+      const GatedTile t = place(s, job);
+      if (CB < 16 && (threadIdx.x & 31) == 0) mbar_arrive(&bars->placed[s]);
+      load(s, t);
+    }
+    // after the tile that ends the CTA nothing is left to place
+    for (int it = 0; reinterpret_cast<const GatedTile*>(smem + SM::kTiles)[it & 3].job < p.jobs; ++it) {
       const int par = it & 1;
-      const uint32_t phase = (it >> 1) & 1;
-      int job = 0;  // of tile it + 2; its latency is hidden by what follows
-      if (lane == 0) job = gated_next(p, tiles[(it + 1) & 3].job);
-      if (CB < 16) place(it + 2, __shfl_sync(0xffffffffu, job, 0));  // the workers load it once past `entered`
-      const bool active = lane < kChan && t.c0 + lane < p.channels;
-      const int64_t row = (int64_t)t.b * p.channels + t.c0 + lane;
-      float* in = reinterpret_cast<float*>(smem + SM::kEnter) + par * 2 * kChan;
-      if constexpr (BACKWARD) {
-        const int64_t at = ((int64_t)t.b * p.blocks + p.blocks - 1 - t.k) * p.channels + t.c0 + lane;
-        if (lane < kChan) in[kChan + lane] = active ? p.ckpt[at] : 0.0f;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->state[par]);
-      }
-      // backward: tile it + 1 goes where tile it - 1 was, once that is read to
-      // the end (before this tile is mapped)
-      bool due = BACKWARD && CB == 16 && it > 0;
-      auto reload = [&] {
-        load(it + 1, tiles[(it + 1) & 3]);
-        due = false;
-      };
-      const uint32_t phase_before = ((it - 1) >> 1) & 1;
-
-      // look for what enters while the workers make the tile's map
-      unsigned long long* rec = p.rec + (int64_t)t.k * stride + t.chain * kChan + ch;
-      const float* start = BACKWARD ? p.dh : p.h0;
-      float h = t.k == 0 && active && start ? start[row] : 0.0f;
-      bool done = !active || t.k == 0;
-      bool known = gated_look_back(rec, t.k, stride, done, h);
-      bool mapped = false;
-      while (!known && !mapped) {  // ends: the workers wait for nothing but loads
-        if (due && all_looked(&bars->freed[par ^ 1], phase_before)) reload();
-        mapped = all_looked(&bars->mapped[par], phase);
-        if (!mapped) known = gated_look_back(rec, t.k, stride, done, h);
-      }
-      auto tell = [&] {
-        if (lane < kChan) in[lane] = h;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->entered[par]);
-      };
-      if (known) tell();
-      if (due) {
-        if (!mapped) gated_wait(p, &bars->freed[par ^ 1], phase_before);
-        reload();
-      }
-      if (!mapped) gated_wait(p, &bars->mapped[par], phase);
-      const float* maps = reinterpret_cast<const float*>(smem + SM::kMaps) + par % SM::kMapSets * SM::kMapSet;
-      float tp, th;
-      gated_fold<kChan, BACKWARD>(maps, maps + (BACKWARD ? 2 : 1) * SM::kPlane, ch, tp, th);
-      const bool more = active && t.k + 1 < p.blocks;
-      if (!known) {
-        if (more) rec_put(rec, tp, th);
-        uint64_t t0 = 0;
-        for (uint32_t round = 0; !gated_look_back(rec, t.k, stride, done, h); ++round) {
-          if ((round & 63u) == 63u) {
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (__any_sync(0xffffffffu, now - t0 > gated_limit(p))) {
-              record_device_error(MAMBA_ERR_TIMEOUT);
-              break;
-            }
-          }
-        }
-        tell();
-      }
-      // what leaves, rounded as a reader of (P, H) rounds it
-      const float after = fmaf(tp, h, th);
-      if (more) rec_put(rec, 0.0f, after);
-      if (active) {
-        if (!BACKWARD && p.ckpt) p.ckpt[((int64_t)t.b * p.blocks + t.k) * p.channels + t.c0 + lane] = h;
-        float* out = BACKWARD ? p.dh0 : p.final_state;
-        if (t.k + 1 == p.blocks && out) out[row] = after;
-      }
-      if (CB == 16) {
-        const GatedTile ahead = place(it + 2, __shfl_sync(0xffffffffu, job, 0));
-        if (!BACKWARD) load(it + 2, ahead);  // the stage is read: its tile is mapped
-      }
+      gated_wait(p, BACKWARD ? &bars->freed[par] : &bars->mapped[par], (it >> 1) & 1);
+      const GatedTile t = place(it + 2, job);
+      job = min(job + (int)gridDim.x, p.jobs);
+      if (CB < 16 && (threadIdx.x & 31) == 0) mbar_arrive(&bars->placed[par]);
+      load(it + 2, t);
     }
   }
 };
 
-// What both kernels' CTAs start with; true for the control warp, which is then done.
-template <typename TIO, bool BACKWARD, int CB, typename Load>
-__device__ __forceinline__ bool gated_begin(const GatedArgs& p, unsigned char* smem, const CUtensorMap* gate,
-                                            const CUtensorMap* x, const CUtensorMap* dy, Load&& load) {
+// ---------------------------------------------------------------------------
+// carrier warp: works out what enters and what leaves tiles, a lane per channel
+// ---------------------------------------------------------------------------
+template <typename TIO, bool BACKWARD>
+__device__ __forceinline__ void gated_carry(const GatedArgs& p, unsigned char* smem, GatedBars* bars) {
   using SM = GatedSmem<TIO, BACKWARD>;
-  GatedBars* bars = reinterpret_cast<GatedBars*>(smem + SM::kBars);
-  GatedTile* tiles = reinterpret_cast<GatedTile*>(smem + SM::kTiles);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->full[i], CB == 16 ? 1 : kGatedWorkers);
-      mbar_init(&bars->mapped[i], kGatedWorkers / 32);
-      mbar_init(&bars->entered[i], 1);
-      mbar_init(&bars->state[i], 1);
-      mbar_init(&bars->freed[i], kGatedWorkers / 32);
+  constexpr int kChan = SM::kChan;
+  const int lane = threadIdx.x & 31, ch = lane < kChan ? lane : 0;
+  const int64_t stride = (int64_t)p.chains * kChan;
+  for (int it = 0;; ++it) {
+    const int par = it & 1;
+    const uint32_t phase = (it >> 1) & 1;
+    gated_wait(p, &bars->full[par], phase);
+    const GatedTile t = reinterpret_cast<const GatedTile*>(smem + SM::kTiles)[it & 3];
+    if (t.job >= p.jobs) return;
+    const bool active = lane < kChan && t.c0 + lane < p.channels;
+    const int64_t row = (int64_t)t.b * p.channels + t.c0 + lane;
+    unsigned long long* rec = p.rec + (int64_t)t.k * stride + t.chain * kChan + ch;
+    const float* start = BACKWARD ? p.dh : p.h0;
+    float h = t.k == 0 && active && start ? start[row] : 0.0f;
+    float* in = reinterpret_cast<float*>(smem + SM::kEnter) + par * 2 * kChan;
+    auto tell = [&] {
+      if (lane < kChan) in[lane] = h;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->entered[par]);
+    };
+    // looks for what enters while the workers make the tile's map
+    GatedLook look;
+    bool done = !active || t.k == 0, mapped = false;
+    bool known = __all_sync(0xffffffffu, done);
+    while (!known && !mapped) {  // ends: the workers wait for nothing but loads
+      look.ask(rec, t.k, stride, done);
+      mapped = __all_sync(0xffffffffu, mbar_test_wait(&bars->mapped[par], phase));
+      if (!mapped) known = look.found(done, h);
     }
-    fence_mbar_init();
-  }
-  griddep_launch_dependents();
-  griddep_wait();
-  __syncthreads();
-  const bool control = threadIdx.x >= kGatedWorkers;
-  GatedControl<TIO, BACKWARD, CB> c{p, smem, bars, tiles, gate, x, dy};
-  if (control) c.first();
-  if (CB < 16) {
-    __syncthreads();
-    if (!control) {
-#pragma unroll
-      for (int s = 0; s < kGatedStages; ++s) load(s);
+    if (known) {
+      tell();
+      gated_wait(p, &bars->mapped[par], phase);
+    }
+    const float* maps = reinterpret_cast<const float*>(smem + SM::kMaps) + par % SM::kMapSets * SM::kMapSet;
+    float tp, th;
+    gated_fold<kChan, BACKWARD>(maps, maps + (BACKWARD ? 2 : 1) * SM::kPlane, ch, tp, th);
+    const bool more = active && t.k + 1 < p.blocks;
+    if (!known) {
+      if (more) rec_put(rec, tp, th);
+      uint64_t t0 = 0;
+      for (uint32_t round = 0; !look.found(done, h); ++round) {
+        look.ask(rec, t.k, stride, done);
+        if ((round & 63u) == 63u) {
+          const uint64_t now = globaltimer_ns();
+          if (t0 == 0) t0 = now;
+          if (__any_sync(0xffffffffu, now - t0 > gated_limit(p))) {
+            record_device_error(MAMBA_ERR_TIMEOUT);
+            break;
+          }
+        }
+      }
+      tell();
+    }
+    // what leaves, rounded as a reader of (P, H) rounds it
+    const float after = fmaf(tp, h, th);
+    if (more) rec_put(rec, 0.0f, after);
+    if (active) {
+      if (!BACKWARD && p.ckpt) p.ckpt[((int64_t)t.b * p.blocks + t.k) * p.channels + t.c0 + lane] = h;
+      float* out = BACKWARD ? p.dh0 : p.final_state;
+      if (t.k + 1 == p.blocks && out) out[row] = after;
     }
   }
-  if (control) c.run();
-  return control;
 }
 
 // A worker's part of loading tile `it` where there is no TMA
@@ -598,6 +554,7 @@ __device__ __forceinline__ void gated_worker_load(const GatedArgs& p, unsigned c
     const int stage = it % kGatedStages;
     GatedBars* bars = reinterpret_cast<GatedBars*>(smem + SM::kBars);
     const GatedTile& t = reinterpret_cast<const GatedTile*>(smem + SM::kTiles)[it & 3];
+    gated_wait(p, &bars->placed[stage], (it / kGatedStages) & 1);
     if (t.job < p.jobs) {
       const int width = (int)min((int64_t)kGatedRow, (p.channels - t.c0) * kES);
       const int64_t pitch = p.channels * kES;
@@ -610,6 +567,39 @@ __device__ __forceinline__ void gated_worker_load(const GatedArgs& p, unsigned c
     if (CB == 4) gated_arrive_async(&bars->full[stage]);
     else mbar_arrive(&bars->full[stage]);
   }
+}
+
+// What both kernels' CTAs start with; false for the carrier and the loader, which
+// are then done.
+template <typename TIO, bool BACKWARD, int CB>
+__device__ __forceinline__ bool gated_begin(const GatedArgs& p, unsigned char* smem, const CUtensorMap* gate,
+                                            const CUtensorMap* x, const CUtensorMap* dy) {
+  using SM = GatedSmem<TIO, BACKWARD>;
+  GatedBars* bars = reinterpret_cast<GatedBars*>(smem + SM::kBars);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->full[i], (CB == 16 ? 1 : kGatedWorkers) + (BACKWARD ? 1 : 0));
+      mbar_init(&bars->mapped[i], kGatedWorkers / 32);
+      mbar_init(&bars->entered[i], 1);
+      mbar_init(&bars->freed[i], kGatedWorkers / 32);
+      mbar_init(&bars->placed[i], 1);
+    }
+    fence_mbar_init();
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+  __syncthreads();
+  if (threadIdx.x >= kGatedWorkers + 32) {
+    GatedLoader<TIO, BACKWARD, CB>{p, smem, bars, gate, x, dy}.run();
+    return false;
+  }
+  if (threadIdx.x >= kGatedWorkers) {
+    gated_carry<TIO, BACKWARD>(p, smem, bars);
+    return false;
+  }
+#pragma unroll
+  for (int s = 0; s < kGatedStages; ++s) gated_worker_load<TIO, BACKWARD, CB>(p, smem, s);
+  return true;
 }
 
 __device__ __forceinline__ void gated_warp_arrive(uint64_t* bar) {
@@ -630,7 +620,7 @@ gated_scan_kernel(const GatedArgs p, const __grid_constant__ CUtensorMap map_gat
   extern __shared__ __align__(128) unsigned char gated_smem[];
   unsigned char* smem = gated_smem;
   auto load = [&](int it) { gated_worker_load<TIO, false, CB>(p, smem, it); };
-  if (gated_begin<TIO, false, CB>(p, smem, &map_gate, &map_x, &map_dy, load)) return;
+  if (!gated_begin<TIO, false, CB>(p, smem, &map_gate, &map_x, &map_dy)) return;
   GatedBars* bars = reinterpret_cast<GatedBars*>(smem + SM::kBars);
   const int tid = threadIdx.x, seg = tid >> 4, col = (tid & 15) * V;
   const uint32_t mine = smem_addr(smem) + seg * kGatedSegBytes + (tid & 15) * 4;
@@ -718,7 +708,7 @@ gated_backward_kernel(const GatedArgs p, const __grid_constant__ CUtensorMap map
   extern __shared__ __align__(128) unsigned char gated_smem[];
   unsigned char* smem = gated_smem;
   auto load = [&](int it) { gated_worker_load<TIO, true, CB>(p, smem, it); };
-  if (gated_begin<TIO, true, CB>(p, smem, &map_gate, &map_x, &map_dy, load)) return;
+  if (!gated_begin<TIO, true, CB>(p, smem, &map_gate, &map_x, &map_dy)) return;
   GatedBars* bars = reinterpret_cast<GatedBars*>(smem + SM::kBars);
   const int tid = threadIdx.x, seg = tid >> 4, col = (tid & 15) * V;
   const uint32_t mine = smem_addr(smem) + seg * kGatedSegBytes + (tid & 15) * 4;
@@ -774,7 +764,6 @@ gated_backward_kernel(const GatedArgs p, const __grid_constant__ CUtensorMap map
     gated_put<V>(seg_r + seg * kChan, R);
     gated_warp_arrive(&bars->mapped[par]);
     gated_wait(p, &bars->mapped[par], phase);
-    gated_wait(p, &bars->state[par], phase);
 
     // b becomes h_{t-1} (minus x_t when convex)
     const float* enter = reinterpret_cast<const float*>(smem + SM::kEnter) + par * 2 * kChan + col;

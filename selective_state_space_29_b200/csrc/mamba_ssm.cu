@@ -882,10 +882,25 @@ int launch_gated_pass(const GatedArgs& p, const CUtensorMap (&maps)[3], cudaStre
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes) != cudaSuccess)
     return MAMBA_ERR_CUDA;
   const unsigned ctas = (unsigned)std::min<int64_t>(p.jobs, 2 * (int64_t)sms);
-  return launch_pdl(kernel, dim3(ctas), dim3(kGatedThreads), (size_t)kBytes, stream, p, maps[0], maps[1], maps[2]) ==
-                 cudaSuccess
-             ? MAMBA_OK
-             : MAMBA_ERR_CUDA;
+  // With several tiles of time the CTAs wait for one another: a cooperative
+  // launch has them all on the GPU at once, or fails.  Else the kernel may
+  // start while the stream's previous one ends.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kGatedThreads);
+  cfg.dynamicSmemBytes = (size_t)kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  if (p.blocks > 1) {
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, maps[0], maps[1], maps[2]) == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA;
 }
 
 int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int dtype, cudaStream_t stream) {
@@ -910,29 +925,29 @@ int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int 
   CUtensorMap maps[3];
   std::memset(maps, 0, sizeof(maps));
   if (cb == 16) {
+    // the largest box that reads less than a sixteenth of a sequence past its
+    // end (a box is one instruction of the loader's)
+    for (p.box = kGatedBlock; p.box > 32 && 16 * ((p.len + p.box - 1) / p.box * p.box - p.len) > p.len; p.box /= 2) {
+    }
     const void* from[3] = {p.gate, p.x, p.dy};
     for (int i = 0; i < (backward ? 3 : 2); ++i)
       if (!make_map_2d(&maps[i], from[i], dtype, (uint64_t)p.channels, (uint64_t)(batch * p.len), (uint32_t)chan,
-                       kGatedBox))
+                       (uint32_t)p.box))
         cb = 4;
   }
-  // scratch: records and a counter for every pass over several tiles of time,
-  // and the checkpoints that a backward call has not been given
+  // scratch: records for every pass over several tiles of time, and the
+  // checkpoints that a backward call has not been given
   const bool own_ckpt = backward && !p.ckpt;
-  const size_t pass = blocks > 1 ? ((size_t)p.jobs * chan + 2) * sizeof(unsigned long long) : 0;
+  const size_t pass = blocks > 1 ? (size_t)p.jobs * chan * sizeof(unsigned long long) : 0;
   const size_t passes = pass * (own_ckpt ? 2 : 1);
   const size_t ck = own_ckpt ? (size_t)batch * blocks * p.channels * sizeof(float) : 0;
   unsigned char* mem = nullptr;
   if (passes + ck > 0 && scratch_alloc(reinterpret_cast<void**>(&mem), passes + ck, stream) != cudaSuccess)
     return MAMBA_ERR_CUDA;
   int st = MAMBA_OK;
-  // records not yet written, counters one before the first tile
   if (passes > 0 && cudaMemsetAsync(mem, 0xff, passes, stream) != cudaSuccess) st = MAMBA_ERR_CUDA;
   auto scratch_of = [&](GatedArgs q, int i) {
-    if (pass > 0) {
-      q.ticket = reinterpret_cast<int*>(mem + i * pass);
-      q.rec = reinterpret_cast<unsigned long long*>(mem + i * pass) + 2;
-    }
+    if (pass > 0) q.rec = reinterpret_cast<unsigned long long*>(mem + i * pass);
     return q;
   };
   auto run = [&](auto cbc) {
