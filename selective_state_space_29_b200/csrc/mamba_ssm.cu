@@ -979,60 +979,86 @@ int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int 
 }
 
 // --- layer norm (norm.cuh) -----------------------------------------------------
-// f(element type, elements per vector): 16-byte vectors where every tensor and
-// every row is aligned to them, else single elements
+// f(element type, elements of a vector, shifted): 16-byte vectors where the
+// tensors lie alike, shifted where a row is not aligned to them
 template <typename F>
-int dispatch_norm(int dtype, bool vec, F&& f) {
+int dispatch_norm(NormArgs& p, int dtype, const void* a, const void* b, const void* c, F&& f) {
+  const int es = elem_size(dtype);
+  auto off = [](const void* q) { return (int)(reinterpret_cast<uintptr_t>(q) % 16); };
+  const bool alike = off(a) == off(b) && off(a) == off(c) && (int64_t)p.channels * es >= 64;
+  const bool shift = off(a) != 0 || (int64_t)p.channels * es % 16 != 0;
+  p.shift0 = off(a) / es;
+  p.period = alike && shift ? 16 / es : 1;
   using One = std::integral_constant<int, 1>;
-  if (dtype == MAMBA_BF16)
-    return vec ? f(__nv_bfloat16{}, std::integral_constant<int, 8>{}) : f(__nv_bfloat16{}, One{});
-  return vec ? f(float{}, std::integral_constant<int, 4>{}) : f(float{}, One{});
+  using T = std::true_type;
+  using N = std::false_type;
+  if (dtype == MAMBA_BF16) {
+    using E = std::integral_constant<int, 8>;
+    return !alike ? f(__nv_bfloat16{}, One{}, N{}) : shift ? f(__nv_bfloat16{}, E{}, T{}) : f(__nv_bfloat16{}, E{}, N{});
+  }
+  using E = std::integral_constant<int, 4>;
+  return !alike ? f(float{}, One{}, N{}) : shift ? f(float{}, E{}, T{}) : f(float{}, E{}, N{});
 }
 
-// lanes per row (log2, 4 to 512 lanes) that hold `vecs` vectors at `per` each
-int norm_lanes_log2(int64_t vecs, int64_t per) {
-  int l = 2;
-  while ((int64_t(1) << l) * per < vecs && l < 9) ++l;
-  return l;
+// Threads of a row of `vecs` vectors, vpt each; rows of a CTA of 256 threads at a time
+void norm_lanes(NormArgs& p, int64_t vecs, int vpt) {
+  const int64_t lanes = (vecs + vpt - 1) / vpt;
+  if (lanes > 16) {
+    p.lanes = (int)((lanes + 31) / 32 * 32);
+  } else {
+    p.lanes = 1;
+    while (p.lanes < lanes) p.lanes *= 2;
+  }
+  p.groups = std::max(1, 256 / p.lanes);
 }
 
-template <typename TIO, int E>
+template <typename TIO, int E, bool SHIFT>
 int launch_norm(NormArgs p, cudaStream_t stream) {
   int sms = 0;
   if (int st = current_sms(&sms)) return st;
-  const int64_t vecs = (p.channels + E - 1) / E;
-  auto run = [&](auto vpl) -> int {
-    constexpr int VPL = decltype(vpl)::value;
-    p.lr_log2 = norm_lanes_log2(vecs, VPL);
-    const int threads = std::max(256, 1 << p.lr_log2);
-    const int64_t slots = threads >> p.lr_log2, ctas = (p.rows + slots - 1) / slots;
-    return launch_pdl(norm_kernel<TIO, E, VPL>, dim3((unsigned)ctas), dim3(threads), 0, stream, p) == cudaSuccess
+  const int64_t vecs = ((int64_t)p.channels + (SHIFT ? E - 1 : 0) + E - 1) / E;
+  auto run = [&](auto vpt, auto rt, auto th) -> int {
+    constexpr int VPT = decltype(vpt)::value, RT = decltype(rt)::value, THREADS = decltype(th)::value;
+    norm_lanes(p, vecs, VPT);
+    const int64_t each = (int64_t)p.groups * RT * p.period, ctas = (p.rows + each - 1) / each * p.period;
+    return launch_pdl(norm_kernel<TIO, E, VPT, RT, SHIFT, THREADS>, dim3((unsigned)ctas), dim3(p.lanes * p.groups), 0,
+                      stream, p) == cudaSuccess
                ? MAMBA_OK
                : MAMBA_ERR_CUDA;
   };
-  constexpr int K = E == 1 ? 4 : 1;  // single elements: four times the vectors a lane
-  // the most vectors a lane that still leave the SMs 1,024 lanes each
-  auto fills = [&](int per) { return (p.rows << norm_lanes_log2(vecs, per)) >= (int64_t)sms * 1024; };
-  if (vecs > 4 * K * 512 || fills(8 * K)) return run(std::integral_constant<int, 8 * K>{});
-  if (vecs > 2 * K * 512 || fills(4 * K)) return run(std::integral_constant<int, 4 * K>{});
-  return run(std::integral_constant<int, 2 * K>{});
+  using std::integral_constant;
+  using T256 = integral_constant<int, 256>;
+  using T1024 = integral_constant<int, 1024>;
+  // 32 elements a thread (16 where they go one by one): as few of a row, and as
+  // many rows, as CTAs of 256 threads take; few rows, one of them a thread
+  constexpr int V = E == 1 ? 16 : 32 / E, K = E == 1 ? 2 : 1;
+  if (p.rows < (int64_t)sms * 8) {
+    if (vecs <= K * 256) return run(integral_constant<int, K>{}, integral_constant<int, 1>{}, T256{});
+    if (vecs <= K * 1024) return run(integral_constant<int, K>{}, integral_constant<int, 1>{}, T1024{});
+  } else {
+    if (vecs <= K * 256) return run(integral_constant<int, K>{}, integral_constant<int, V / K>{}, T256{});
+    if (vecs <= 4 * K * 256) return run(integral_constant<int, 4 * K>{}, integral_constant<int, V / K / 4>{}, T256{});
+  }
+  if (vecs <= 8 * K * 256) return run(integral_constant<int, 8 * K>{}, integral_constant<int, 1>{}, T256{});
+  return run(integral_constant<int, 8 * K>{}, integral_constant<int, 1>{}, T1024{});
 }
 
-template <typename TIO, int E>
+template <typename TIO, int E, bool SHIFT>
 int launch_norm_backward(NormArgs p, cudaStream_t stream) {
   int sms = 0;
   if (int st = current_sms(&sms)) return st;
-  const int64_t vecs = (p.channels + E - 1) / E;
-  auto run = [&](auto vpl) -> int {
-    constexpr int VPL = decltype(vpl)::value;
-    p.lr_log2 = norm_lanes_log2(vecs, VPL);
-    const int threads = kNormMaxThreads;
-    const int64_t slots = threads >> p.lr_log2;
-    const int ctas = (int)std::min<int64_t>(sms, (p.rows + slots - 1) / slots);
-    const size_t smem = (size_t)threads * VPL * E * sizeof(float);
-    auto kernel = norm_backward_kernel<TIO, E, VPL>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  const int64_t vecs = ((int64_t)p.channels + (SHIFT ? E - 1 : 0) + E - 1) / E;
+  auto run = [&](auto vpt, auto rt, auto th) -> int {
+    constexpr int VPT = decltype(vpt)::value, RT = decltype(rt)::value, THREADS = decltype(th)::value;
+    auto kernel = norm_backward_kernel<TIO, E, VPT, RT, SHIFT, THREADS>;
+    norm_lanes(p, vecs, VPT);
+    const int threads = p.lanes * p.groups;
+    const size_t smem = p.groups > 1 ? (size_t)p.groups * p.channels * sizeof(float) : 0;
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
       return MAMBA_ERR_CUDA;
+    const int64_t each = (int64_t)p.groups * RT * p.period;
+    const int ctas = (int)std::min<int64_t>((p.rows + each - 1) / each, std::max(1, sms * per_sm / p.period)) * p.period;
     unsigned char* mem = nullptr;
     if (p.dweight || p.dbias) {
       if (scratch_alloc(reinterpret_cast<void**>(&mem), (size_t)ctas * 2 * p.channels * sizeof(float), stream) !=
@@ -1048,9 +1074,18 @@ int launch_norm_backward(NormArgs p, cudaStream_t stream) {
     if (mem && cudaFreeAsync(mem, stream) != cudaSuccess && st == MAMBA_OK) st = MAMBA_ERR_CUDA;
     return st;
   };
-  // a lane holds 16 elements (32 in the longest rows)
-  if (vecs * E > 16 * kNormMaxThreads) return run(std::integral_constant<int, 32 / E>{});
-  return run(std::integral_constant<int, 16 / E>{});
+  using std::integral_constant;
+  using T256 = integral_constant<int, 256>;
+  using T1024 = integral_constant<int, 1024>;
+  constexpr int K = E == 1 ? 4 : 1;
+#ifndef NB_RT
+#define NB_RT 4
+#endif
+  if (vecs <= K * 256 && p.rows >= (int64_t)sms * 8) return run(integral_constant<int, K>{}, integral_constant<int, NB_RT>{}, T256{});
+  if (vecs <= K * 256) return run(integral_constant<int, K>{}, integral_constant<int, 1>{}, T256{});
+  if (vecs <= 2 * K * 256) return run(integral_constant<int, 2 * K>{}, integral_constant<int, 2>{}, T256{});
+  if (vecs <= 4 * K * 256) return run(integral_constant<int, 4 * K>{}, integral_constant<int, 1>{}, T256{});
+  return run(integral_constant<int, 8 * K>{}, integral_constant<int, 1>{}, T1024{});
 }
 
 }  // namespace
@@ -1721,12 +1756,10 @@ int mamba_layer_norm(const void* x, const float* weight, const float* bias, void
   p.rstd = rstd;
   p.rows = rows;
   p.channels = (int)channels;
-  p.wide = aligned(weight, 16) && aligned(bias, 16);
   p.rms = (flags & MAMBA_NORM_RMS) ? 1 : 0;
   p.eps = eps;
-  const bool vec = (channels * (int64_t)es) % 16 == 0 && aligned(x, 16) && aligned(y, 16);
-  return dispatch_norm(dtype, vec, [&](auto tio, auto e) {
-    return launch_norm<decltype(tio), decltype(e)::value>(p, stream);
+  return dispatch_norm(p, dtype, x, y, y, [&](auto tio, auto e, auto shift) {
+    return launch_norm<decltype(tio), decltype(e)::value, decltype(shift)::value>(p, stream);
   });
 }
 
@@ -1768,11 +1801,9 @@ int mamba_layer_norm_backward(const void* dy, const void* x, const float* weight
   p.dbias = dbias;
   p.rows = rows;
   p.channels = (int)channels;
-  p.wide = aligned(weight, 16);
   p.rms = rms;
-  const bool vec = (channels * (int64_t)es) % 16 == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(dx, 16);
-  return dispatch_norm(dtype, vec, [&](auto tio, auto e) {
-    return launch_norm_backward<decltype(tio), decltype(e)::value>(p, stream);
+  return dispatch_norm(p, dtype, x, dy, dx, [&](auto tio, auto e, auto shift) {
+    return launch_norm_backward<decltype(tio), decltype(e)::value, decltype(shift)::value>(p, stream);
   });
 }
 

@@ -6,290 +6,476 @@
 //     dweight = sum over rows of dy xh,  dbias = sum over rows of dy
 //
 // Both directions are bound by HBM: 4 bytes an element forward and 6 backward
-// (bf16), each read once into registers and held there for the sums and the
-// outputs.  A row is held by LR lanes, a power of two from 4 to 512, each with
-// VPL vectors of E elements (16 bytes, or one element where rows are not
-// 16-byte aligned); sums go by shuffles, and through shared memory where a row
-// has several warps.
+// (bf16), each read once.  A thread takes VPT vectors of channels through RT
+// rows, all of them loaded into registers, as they are, before anything else:
+// weight and bias, and the sums of their gradients, are then shared by RT rows
+// (with a row to a warp they are read again for every row, and cost L1 twice
+// the row's own bytes), and so are the meetings of a row's warps.  The RT rows'
+// sums go over the lanes together: each exchange halves the number of sums a
+// lane holds, 7 exchanges for 8 sums in place of 40.
+//   forward:  one CTA to a few rows, many CTAs to an SM.
+//   backward: CTAs walk the rows, hold the next ones while they work on these,
+//             and keep the sums of the weight's and bias' gradients in
+//             registers; a second kernel joins the CTAs' sums in order.
+// Vectors are 16 bytes.  SHIFT: rows that are not 16-byte aligned are covered by
+// aligned vectors that start up to E - 1 elements before them, the ones at a
+// row's ends by elements; a CTA's rows are a multiple of E apart, so that all
+// of them have one shift.  Tensors that are not aligned alike: single elements.
 #pragma once
 
 #include "common.cuh"
 
 namespace mamba {
 
-// E elements of TIO, as loaded
-template <typename TIO, int E>
-struct NormVec {
-  static_assert(E == 1 || E * sizeof(TIO) == 16, "one element or 16 bytes");
-  uint32_t w[E == 1 ? 1 : 4];
-  __device__ __forceinline__ void load(const TIO* p) {
-    if constexpr (E == 1) {
-      if constexpr (sizeof(TIO) == 4) w[0] = __float_as_uint(__ldg(p));
-      else w[0] = (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16;
-    } else {
-      // read once: kept out of L1, which holds weight and bias
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                   : "l"(p));
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < (E == 1 ? 1 : 4); ++i) w[i] = 0u;
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (E == 1 || sizeof(TIO) == 4) return __uint_as_float(w[i]);
-    else return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-  }
-};
-
-template <typename TIO, int E>
-__device__ __forceinline__ void norm_store(TIO* p, const float (&v)[E]) {
-  if constexpr (E == 1) {
-    *p = from_f32<TIO>(v[0]);
-  } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(TIO) == 4) w[i] = __float_as_uint(v[i]);
-      else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
-// E float32 parameters (weight, bias), or `none` where there are none
-template <int E>
-__device__ __forceinline__ void norm_param(const float* p, int64_t at, float none, bool wide, float (&v)[E]) {
-  if (p == nullptr) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = none;
-  } else if (E >= 4 && wide) {
-#pragma unroll
-    for (int i = 0; i + 3 < E; i += 4) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(p + at + i));
-      v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = __ldg(p + at + i);
-  }
-}
-
-// Sums of K values over the LR lanes of a row, in every lane.  `sh` has K
-// floats per warp; rows of several warps meet at barrier `bar` (their lanes
-// only), which also closes the previous use of the other half of `sh`.
-template <int K>
-__device__ __forceinline__ void norm_row_sum(float (&v)[K], int lr, float* sh, int bar) {
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    for (int o = 1; o < lr && o < 32; o <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  }
-  if (lr > 32) {
-    const int warps = lr >> 5, warp = threadIdx.x >> 5, first = warp & ~(warps - 1);
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) sh[warp * K + k] = v[k];
-    }
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(lr) : "memory");
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = 0.0f;
-    for (int w = 0; w < warps; ++w) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += sh[(first + w) * K + k];
-    }
-  }
-}
-
 struct NormArgs {
   const void* x;
   const void* dy;
   const float* weight;
   const float* bias;
-  void* y;             // dx in the backward
+  void* y;               // dx in the backward
   float* mean;
   float* rstd;
   const float* mean_in;
   const float* rstd_in;
-  float* part;         // [ctas][2][channels]: sums of dy xh, dy
+  float* part;           // [ctas][2][channels]: sums of dy xh, dy; NULL: not wanted
   float* dweight;
   float* dbias;
   int64_t rows;
   int channels;
-  int lr_log2;
-  int wide;            // weight and bias 16-byte aligned
+  int lanes;             // threads of a row: a power of two below 32, or whole warps
+  int groups;            // rows of a CTA at a time, RT times
+  int period;            // a thread's rows lie this far apart (see SHIFT)
+  int shift0;            // elements from a 16-byte boundary to the first row
   int rms;
   float eps;
 };
 
-constexpr int kNormMaxThreads = 512;
+__device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
+// a / n, given 1 / n rounded: one step makes up for the rounding
+__device__ __forceinline__ float over(float a, float n, float rcp) {
+  const float q = a * rcp;
+  return fmaf(fmaf(-n, q, a), rcp, q);
+}
+__device__ __forceinline__ float norm_rstd(float var) {
+  float r = rsqrtf(var);  // and one Newton step
+  r = fmaf(0.5f * r, fmaf(-var * r, r, 1.0f), r);
+  return var > 1e-30f && var < 1e30f ? r : 1.0f / sqrtf(var);
+}
 
-template <typename TIO, int E, int VPL>
-__global__ void __launch_bounds__(kNormMaxThreads) norm_kernel(const NormArgs p) {
-  __shared__ float sh[2][kNormMaxThreads / 32];
-  const int lr = 1 << p.lr_log2, slot = threadIdx.x >> p.lr_log2, lane = threadIdx.x & (lr - 1);
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> p.lr_log2) + slot;
-  const bool live = row < p.rows;
-  const TIO* x = static_cast<const TIO*>(p.x) + row * p.channels;
-  const float n = (float)p.channels;
-  griddep_launch_dependents();
-  griddep_wait();
+// Where a thread stands: its vectors of E elements, and the first of its rows
+template <int E, bool SHIFT>
+struct NormPlace {
+  int group, own, lanes, channels, shift;
+  int64_t row;
+  __device__ __forceinline__ NormPlace(const NormArgs& p, int rt) {
+    group = threadIdx.x / p.lanes;
+    own = threadIdx.x - group * p.lanes;
+    lanes = p.lanes;
+    channels = p.channels;
+    const int64_t b = SHIFT ? blockIdx.x / p.period : blockIdx.x;
+    row = (b * p.groups + group) * rt;
+    if (SHIFT) row = row * p.period + blockIdx.x % p.period;
+    shift = SHIFT ? (int)((p.shift0 + row * p.channels) % E) : 0;
+  }
+  __device__ __forceinline__ int first(int j) const { return (own + j * lanes) * E - shift; }  // channel
+  __device__ __forceinline__ bool any(int c) const { return c < channels; }                    // of a vector's
+  __device__ __forceinline__ bool whole(int c) const { return !SHIFT || (c >= 0 && c + E <= channels); }
+  __device__ __forceinline__ bool in(int c) const { return !SHIFT || (c >= 0 && c < channels); }  // one of any()
+};
 
-  NormVec<TIO, E> v[VPL];
+// E elements of TIO (16 bytes, or one), as they are in memory
+template <typename TIO, int E>
+struct NormVec {
+  static_assert(E == 1 || E * sizeof(TIO) == 16, "one element or 16 bytes");
+  static constexpr int kP = (E + 1) / 2, kW = E == 1 ? 1 : 4;
+  uint32_t w[kW];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int c = (lane + (j << p.lr_log2)) * E;
-    if (live && c < p.channels) v[j].load(x + c);
-    else v[j].zero();
+    for (int i = 0; i < kW; ++i) w[i] = 0u;
   }
-  float mean = 0.0f;
-  if (!p.rms) {
-    float s[1] = {0.0f};
+  // hides that the words are those of before, so that their floats are not kept beside them
+  __device__ __forceinline__ void again() {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-#pragma unroll
-      for (int e = 0; e < E; ++e) s[0] += v[j].get(e);
-    norm_row_sum<1>(s, lr, sh[0], 1 + slot);
-    mean = s[0] / n;
+    for (int i = 0; i < kW; ++i) asm volatile("" : "+r"(w[i]));
   }
-  float q[1] = {0.0f};
+  static __device__ __forceinline__ uint32_t raw(const TIO* p) {
+    if constexpr (sizeof(TIO) == 4) return __float_as_uint(__ldg(p));
+    else return __ldg(reinterpret_cast<const unsigned short*>(p));
+  }
+  template <typename Place>
+  __device__ __forceinline__ void load(const Place& at, int c, const TIO* p) {
+    if constexpr (E == 1) {
+      w[0] = sizeof(TIO) == 4 ? raw(p) : raw(p) << 16;
+    } else if (at.whole(c)) {
+      // read once: kept out of L1, which holds weight and bias
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "l"(p));
+    } else {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    if ((lane + (j << p.lr_log2)) * E < p.channels) {
+      for (int e = 0; e < E; ++e)
+        if (at.in(c + e)) {
+          if constexpr (sizeof(TIO) == 4) w[e] = raw(p + e);
+          else w[e / 2] |= raw(p + e) << (16 * (e & 1));
+        }
+    }
+  }
+  // as pairs of floats (one element: y = 0)
+  __device__ __forceinline__ void get(float2 (&v)[kP]) const {
+    if constexpr (E == 1) {
+      v[0] = make_float2(__uint_as_float(w[0]), 0.0f);
+    } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float d = v[j].get(e) - mean;
-        q[0] = fmaf(d, d, q[0]);
+      for (int i = 0; i < kP; ++i) {
+        if constexpr (sizeof(TIO) == 4) v[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
       }
     }
   }
-  norm_row_sum<1>(q, lr, sh[1], 1 + slot);
-  const float rstd = 1.0f / sqrtf(q[0] / n + p.eps);
-  if (!live) return;
-  if (lane == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
+  static __device__ __forceinline__ uint32_t two(float2 v) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+    return r;
   }
-  TIO* y = static_cast<TIO*>(p.y) + row * p.channels;
+  template <typename Place>
+  static __device__ __forceinline__ void put(const Place& at, int c, TIO* p, const float2 (&v)[kP]) {
+    if constexpr (E == 1) {
+      *p = from_f32<TIO>(v[0].x);
+    } else if (at.whole(c)) {
+      if constexpr (sizeof(TIO) == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      else *reinterpret_cast<uint4*>(p) = make_uint4(two(v[0]), two(v[1]), two(v[2]), two(v[3]));
+    } else {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int c = (lane + (j << p.lr_log2)) * E;
-    if (c < p.channels) {
-      float w[E], b[E], o[E];
-      norm_param<E>(p.weight, c, 1.0f, p.wide, w);
-      norm_param<E>(p.bias, c, 0.0f, p.wide, b);
+      for (int e = 0; e < E; ++e)
+        if (at.in(c + e)) p[e] = from_f32<TIO>((e & 1) ? v[e / 2].y : v[e / 2].x);
+    }
+  }
+  // channels c.. of a float32 array (wide: 16-byte aligned), or `none` without one
+  template <typename Place>
+  static __device__ __forceinline__ void param(const Place& at, const float* p, int c, bool wide, float none,
+                                               float2 (&v)[kP]) {
+    if (p == nullptr) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf((v[j].get(e) - mean) * rstd, w[e], b[e]);
-      norm_store<TIO, E>(y + c, o);
+      for (int i = 0; i < kP; ++i) v[i] = pair_of(none);
+    } else if constexpr (E == 1) {
+      v[0] = make_float2(__ldg(p + c), 0.0f);
+    } else if (wide) {
+#pragma unroll
+      for (int i = 0; i + 1 < kP; i += 2) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(p + c + 2 * i));
+        v[i] = make_float2(f.x, f.y);
+        v[i + 1] = make_float2(f.z, f.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kP; ++i)
+        v[i] = make_float2(at.in(c + 2 * i) ? __ldg(p + c + 2 * i) : 0.0f,
+                           at.in(c + 2 * i + 1) ? __ldg(p + c + 2 * i + 1) : 0.0f);
+    }
+  }
+};
+
+// Sums of N values (a power of two up to 16) over a row's lanes, put through f
+// and handed to every lane.  For all of a CTA's threads.  `part` and `total`
+// have N floats for each warp; calls take turns with two sets of them, so that
+// a set is written again only behind the other call's barriers.
+template <int N, typename F>
+__device__ __forceinline__ void norm_total(float (&v)[N], int lanes, int group, int groups, float* part, float* total,
+                                           F&& f) {
+  if (lanes < 32) {
+    for (int o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = f(i, v[i]);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
+  int at = 0;
+#pragma unroll
+  for (int n = N / 2, o = 16; n >= 1; n /= 2, o /= 2) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+    if (upper) at += n;
+  }
+#pragma unroll
+  for (int o = 16 / N; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  if ((lane & (32 / N - 1)) == 0) part[(threadIdx.x >> 5) * N + at] = v[0];
+  __syncthreads();
+  const int warps = lanes >> 5;
+  for (int k = threadIdx.x; k < groups * N; k += blockDim.x) {
+    const int g = k / N, i = k % N;
+    float t = 0.0f;
+    for (int w = 0; w < warps; ++w) t += part[(g * warps + w) * N + i];
+    total[k] = f(i, t);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = total[group * N + i];
+}
+
+// A thread's vectors of RT rows.  `from` is its first row's first vector; rows
+// lie `pitch` elements apart, and the first `live` of them are rows.
+template <typename TIO, int E, int VPT, int RT, bool SHIFT>
+struct NormTile {
+  using Place = NormPlace<E, SHIFT>;
+  NormVec<TIO, E> v[RT][VPT];
+  __device__ __forceinline__ void load(const Place& at, const TIO* from, int pitch, int live) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        v[i][j].zero();
+        const int c = at.first(j);
+        if (i < live && at.any(c)) v[i][j].load(at, c, from + i * pitch + j * at.lanes * E);
+      }
+  }
+  __device__ __forceinline__ void again() {
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) v[i][j].again();
+  }
+};
+// how many of a thread's rows from `row` on, `period` apart, there are
+__device__ __forceinline__ int norm_live(const NormArgs& p, int64_t row, int rt) {
+  const int64_t left = p.rows - row;
+  return left <= 0 ? 0 : (int)min((int64_t)rt, (left + p.period - 1) / p.period);
+}
+
+template <typename TIO, int E, int VPT, int RT, bool SHIFT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) norm_kernel(const NormArgs p) {
+  using Vec = NormVec<TIO, E>;
+  constexpr int P = Vec::kP;
+  __shared__ float part[2][32 * RT], total[2][32 * RT];
+  const NormPlace<E, SHIFT> at(p, RT);
+  const float n = (float)p.channels, rcp_n = 1.0f / n;
+  const bool wide = !SHIFT && (((uintptr_t)p.weight | (uintptr_t)p.bias) & 15) == 0;
+  const int pitch = p.period * p.channels, live = norm_live(p, at.row, RT);
+  const int64_t first = at.row * p.channels + at.first(0);
+  griddep_launch_dependents();
+  griddep_wait();
+  NormTile<TIO, E, VPT, RT, SHIFT> x;
+  x.load(at, static_cast<const TIO*>(p.x) + first, pitch, live);
+  float mean[RT], rstd[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) mean[i] = 0.0f;
+  if (!p.rms) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      float2 s = pair_of(0.0f);
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        float2 f[P];
+        x.v[i][j].get(f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) s = __fadd2_rn(s, f[k]);
+      }
+      mean[i] = s.x + s.y;
+    }
+    x.again();
+    norm_total(mean, p.lanes, at.group, p.groups, part[0], total[0], [&](int, float t) { return over(t, n, rcp_n); });
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    float2 q = pair_of(0.0f);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float2 f[P];
+      x.v[i][j].get(f);
+      const int c = at.first(j);
+      if (!at.any(c)) continue;
+      if (at.whole(c)) {
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const float2 d = __fadd2_rn(f[k], pair_of(-mean[i]));
+          q = __ffma2_rn(d, d, q);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const float2 d = __fadd2_rn(f[k], make_float2(at.in(c + 2 * k) ? -mean[i] : 0.0f,
+                                                        at.in(c + 2 * k + 1) ? -mean[i] : 0.0f));
+          q = __ffma2_rn(d, d, q);
+        }
+      }
+    }
+    rstd[i] = E == 1 ? q.x : q.x + q.y;
+  }
+  x.again();
+  norm_total(rstd, p.lanes, at.group, p.groups, part[1], total[1],
+             [&](int, float t) { return norm_rstd(over(t, n, rcp_n) + p.eps); });
+  if (at.own == 0) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      if (i < live && p.mean) p.mean[at.row + i * p.period] = mean[i];
+      if (i < live && p.rstd) p.rstd[at.row + i * p.period] = rstd[i];
+    }
+  }
+  TIO* y = static_cast<TIO*>(p.y) + first;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = at.first(j);
+    if (!at.any(c)) continue;
+    float2 w[P], b[P];
+    Vec::param(at, p.weight, c, wide, 1.0f, w);
+    Vec::param(at, p.bias, c, wide, 0.0f, b);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      if (i >= live) continue;
+      float2 f[P];
+      x.v[i][j].get(f);
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        f[k] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[k], pair_of(-mean[i])), pair_of(rstd[i])), w[k], b[k]);
+      Vec::put(at, c, y + i * pitch + j * at.lanes * E, f);
     }
   }
 }
 
-// A CTA per SM walks rows; its lanes keep their channels' weight and sums of
-// dy xh and dy in registers, and hold the next row while they work on this
-// one.  The CTA's rows' sums are joined in shared memory and written to `part`.
-template <typename TIO, int E, int VPL>
-__global__ void __launch_bounds__(kNormMaxThreads) norm_backward_kernel(const NormArgs p) {
-  extern __shared__ float dyn[];
-  __shared__ float sh[2][2 * kNormMaxThreads / 32];
-  const int lr = 1 << p.lr_log2, slot = threadIdx.x >> p.lr_log2, lane = threadIdx.x & (lr - 1);
-  const int slots = blockDim.x >> p.lr_log2;
-  const float n = (float)p.channels;
+#ifndef NB_AHEAD
+#define NB_AHEAD 0
+#endif
+#ifndef NB_MIN
+#define NB_MIN 2
+#endif
+template <typename TIO, int E, int VPT, int RT, bool SHIFT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 && VPT * E <= 8 ? NB_MIN : 1)
+norm_backward_kernel(const NormArgs p) {
+  using Vec = NormVec<TIO, E>;
+  using Tile = NormTile<TIO, E, VPT, RT, SHIFT>;
+  constexpr int P = Vec::kP;
+  constexpr bool kAhead = NB_AHEAD;
+  extern __shared__ __align__(16) float norm_smem[];
+  __shared__ float part[2][32 * 2 * RT], total[2][32 * 2 * RT];
+  const NormPlace<E, SHIFT> at(p, RT);
+  const float n = (float)p.channels, rcp_n = 1.0f / n;
+  const bool wide = !SHIFT && ((uintptr_t)p.weight & 15) == 0;
+  const int pitch = p.period * p.channels;
   griddep_launch_dependents();
   griddep_wait();
-
-  float w[VPL][E], dw[VPL][E], db[VPL][E];
+  float2 dw[VPT][P], db[VPT][P];
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int c = (lane + (j << p.lr_log2)) * E;
-    if (c < p.channels) norm_param<E>(p.weight, c, 1.0f, p.wide, w[j]);
+  for (int j = 0; j < VPT; ++j)
 #pragma unroll
-    for (int e = 0; e < E; ++e) dw[j][e] = db[j][e] = 0.0f;
-  }
-  NormVec<TIO, E> x[VPL], g[VPL];
-  float mean = 0.0f, rstd = 0.0f;
-  auto load = [&](int64_t row) {
-    const bool live = row < p.rows;
+    for (int k = 0; k < P; ++k) dw[j][k] = db[j][k] = pair_of(0.0f);
+  const int64_t first = at.row * p.channels + at.first(0);
+  const TIO* from_x = static_cast<const TIO*>(p.x) + first;
+  const TIO* from_g = static_cast<const TIO*>(p.dy) + first;
+  TIO* dx = static_cast<TIO*>(p.y) + first;
+  Tile ahead_x, ahead_g;
+  float ahead_mean[RT], ahead_rstd[RT];
+  auto load = [&](int64_t row, int live) {
+    ahead_x.load(at, from_x, pitch, live);
+    ahead_g.load(at, from_g, pitch, live);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int c = (lane + (j << p.lr_log2)) * E;
-      if (live && c < p.channels) {
-        x[j].load(static_cast<const TIO*>(p.x) + row * p.channels + c);
-        g[j].load(static_cast<const TIO*>(p.dy) + row * p.channels + c);
-      } else {
-        x[j].zero();
-        g[j].zero();
-      }
+    for (int i = 0; i < RT; ++i) {
+      ahead_mean[i] = i < live && !p.rms ? __ldg(p.mean_in + row + i * p.period) : 0.0f;
+      ahead_rstd[i] = i < live ? __ldg(p.rstd_in + row + i * p.period) : 0.0f;  // 0: no row adds nothing
     }
-    mean = live && !p.rms ? __ldg(p.mean_in + row) : 0.0f;
-    rstd = live ? __ldg(p.rstd_in + row) : 0.0f;
   };
-  const int64_t step = (int64_t)gridDim.x * slots;
-  int64_t row = (int64_t)blockIdx.x * slots + slot;
-  load(row);
-  // every slot takes the same number of rounds, so that whole warps stay together
-  const int64_t rounds = (p.rows - (int64_t)blockIdx.x * slots + step - 1) / step;
-  for (int64_t it = 0; it < rounds; ++it, row += step) {
-    const NormVec<TIO, E>*px = x, *pg = g;
-    NormVec<TIO, E> cx[VPL], cg[VPL];
+  const int64_t step = (int64_t)(gridDim.x / p.period) * p.period * p.groups * RT, stride = step * p.channels;
+  int64_t row = at.row;
+  int live = norm_live(p, row, RT), turn = 0;
+  if (kAhead) load(row, live);
+  // by the CTA's first row, so that its threads stay together
+  for (int64_t r0 = row - (int64_t)at.group * RT * p.period; r0 < p.rows; r0 += step, turn ^= 1) {
+    if (!kAhead) load(row, live);
+    Tile x = ahead_x, g = ahead_g;
+    float mean[RT], rstd[RT], s[2 * RT];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      cx[j] = px[j];
-      cg[j] = pg[j];
-    }
-    const float m = mean, r = rstd;
-    const bool live = row < p.rows;
-    load(it + 1 < rounds ? row + step : p.rows);
-    float s[2] = {0.0f, 0.0f};
+    for (int i = 0; i < RT; ++i) mean[i] = ahead_mean[i], rstd[i] = ahead_rstd[i];
+    const int now = live;
+    row += step;
+    from_x += stride;
+    from_g += stride;
+    live = norm_live(p, row, RT);
+    if (kAhead) load(row, live);
+    float2 s1[RT], s2[RT];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      if ((lane + (j << p.lr_log2)) * E < p.channels) {
+    for (int i = 0; i < RT; ++i) s1[i] = s2[i] = pair_of(0.0f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float gy = cg[j].get(e), xh = (cx[j].get(e) - m) * r, d = gy * w[j][e];
-          s[0] += d;
-          s[1] = fmaf(d, xh, s[1]);
-          dw[j][e] = fmaf(gy, xh, dw[j][e]);
-          db[j][e] += gy;
+    for (int j = 0; j < VPT; ++j) {
+      const int c = at.first(j);
+      if (!at.any(c)) continue;
+      float2 w[P];
+      Vec::param(at, p.weight, c, wide, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        float2 fx[P], fg[P];
+        x.v[i][j].get(fx);
+        g.v[i][j].get(fg);  // 0 outside the row, where nothing is added then
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const float2 xh = __fmul2_rn(__fadd2_rn(fx[k], pair_of(-mean[i])), pair_of(rstd[i]));
+          const float2 d = __fmul2_rn(fg[k], w[k]);
+          s1[i] = __fadd2_rn(s1[i], d);
+          s2[i] = __ffma2_rn(d, xh, s2[i]);
+          dw[j][k] = __ffma2_rn(fg[k], xh, dw[j][k]);
+          db[j][k] = __fadd2_rn(db[j][k], fg[k]);
         }
       }
     }
-    norm_row_sum<2>(s, lr, sh[it & 1], 1 + slot);
-    const float s1 = p.rms ? 0.0f : s[0] / n, s2 = s[1] / n;
-    if (live) {
-      TIO* dx = static_cast<TIO*>(p.y) + row * p.channels;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        const int c = (lane + (j << p.lr_log2)) * E;
-        if (c < p.channels) {
-          float o[E];
+    for (int i = 0; i < RT; ++i) {
+      s[i] = E == 1 ? s1[i].x : s1[i].x + s1[i].y;
+      s[RT + i] = E == 1 ? s2[i].x : s2[i].x + s2[i].y;
+    }
+    x.again();
+    g.again();
+    norm_total(s, p.lanes, at.group, p.groups, part[turn], total[turn],
+               [&](int i, float t) { return p.rms && i < RT ? 0.0f : over(t, n, rcp_n); });
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float xh = (cx[j].get(e) - m) * r;
-            o[e] = r * (fmaf(cg[j].get(e), w[j][e], -s1) - xh * s2);
-          }
-          norm_store<TIO, E>(dx + c, o);
+    for (int j = 0; j < VPT; ++j) {
+      const int c = at.first(j);
+      if (!at.any(c)) continue;
+      float2 w[P];
+      Vec::param(at, p.weight, c, wide, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        if (i >= now) continue;
+        float2 fx[P], fg[P];
+        x.v[i][j].get(fx);
+        g.v[i][j].get(fg);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const float2 xh = __fmul2_rn(__fadd2_rn(fx[k], pair_of(-mean[i])), pair_of(rstd[i]));
+          fx[k] = __fmul2_rn(__ffma2_rn(xh, pair_of(-s[RT + i]), __ffma2_rn(fg[k], w[k], pair_of(-s[i]))),
+                             pair_of(rstd[i]));
         }
+        Vec::put(at, c, dx + i * pitch + j * at.lanes * E, fx);
       }
     }
+    dx += stride;
   }
   if (p.part == nullptr) return;
-  // the slots' sums, one after the other in a fixed order
-  float* part = p.part + (int64_t)blockIdx.x * 2 * p.channels;
-  const int held = lr * VPL * E;  // channels a slot holds
+  // the groups' sums, one after the other in a fixed order
+  float* to = p.part + (int64_t)blockIdx.x * 2 * p.channels;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    __syncthreads();
+  for (int which = 0; which < 2; ++which) {
+    if (p.groups > 1) __syncthreads();
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
+    for (int j = 0; j < VPT; ++j) {
+      const int c = at.first(j);
+      if (!at.any(c)) continue;
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        dyn[slot * held + (lane + (j << p.lr_log2)) * E + e] = k == 0 ? dw[j][e] : db[j][e];
-    __syncthreads();
-    for (int c = threadIdx.x; c < p.channels; c += blockDim.x) {
-      float t = 0.0f;
-      for (int s = 0; s < slots; ++s) t += dyn[s * held + c];
-      part[k * p.channels + c] = t;
+      for (int e = 0; e < E; ++e) {
+        const float2 v = which == 0 ? dw[j][e / 2] : db[j][e / 2];
+        if (at.in(c + e))
+          (p.groups > 1 ? norm_smem + at.group * p.channels : to + which * p.channels)[c + e] = (e & 1) ? v.y : v.x;
+      }
+    }
+    if (p.groups > 1) {
+      __syncthreads();
+      for (int c = threadIdx.x; c < p.channels; c += blockDim.x) {
+        float t = 0.0f;
+        for (int k = 0; k < p.groups; ++k) t += norm_smem[k * p.channels + c];
+        to[which * p.channels + c] = t;
+      }
     }
   }
 }
