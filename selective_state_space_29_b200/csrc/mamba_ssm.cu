@@ -1048,16 +1048,19 @@ int launch_norm_backward(NormArgs p, cudaStream_t stream) {
   int sms = 0;
   if (int st = current_sms(&sms)) return st;
   const int64_t vecs = ((int64_t)p.channels + (SHIFT ? E - 1 : 0) + E - 1) / E;
-  auto run = [&](auto vpt, auto rt, auto th) -> int {
-    constexpr int VPT = decltype(vpt)::value, RT = decltype(rt)::value, THREADS = decltype(th)::value;
-    auto kernel = norm_backward_kernel<TIO, E, VPT, RT, SHIFT, THREADS>;
+  auto run = [&](auto vpt, auto th) -> int {
+    constexpr int VPT = decltype(vpt)::value, THREADS = decltype(th)::value;
+    auto kernel = norm_backward_kernel<TIO, E, VPT, SHIFT, THREADS>;
     norm_lanes(p, vecs, VPT);
     const int threads = p.lanes * p.groups;
     const size_t smem = p.groups > 1 ? (size_t)p.groups * p.channels * sizeof(float) : 0;
+    if (smem > 32 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return MAMBA_ERR_CUDA;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
       return MAMBA_ERR_CUDA;
-    const int64_t each = (int64_t)p.groups * RT * p.period;
+    const int64_t each = (int64_t)p.groups * p.period;
     const int ctas = (int)std::min<int64_t>((p.rows + each - 1) / each, std::max(1, sms * per_sm / p.period)) * p.period;
     unsigned char* mem = nullptr;
     if (p.dweight || p.dbias) {
@@ -1075,17 +1078,11 @@ int launch_norm_backward(NormArgs p, cudaStream_t stream) {
     return st;
   };
   using std::integral_constant;
-  using T256 = integral_constant<int, 256>;
-  using T1024 = integral_constant<int, 1024>;
-  constexpr int K = E == 1 ? 4 : 1;
-#ifndef NB_RT
-#define NB_RT 4
-#endif
-  if (vecs <= K * 256 && p.rows >= (int64_t)sms * 8) return run(integral_constant<int, K>{}, integral_constant<int, NB_RT>{}, T256{});
-  if (vecs <= K * 256) return run(integral_constant<int, K>{}, integral_constant<int, 1>{}, T256{});
-  if (vecs <= 2 * K * 256) return run(integral_constant<int, 2 * K>{}, integral_constant<int, 2>{}, T256{});
-  if (vecs <= 4 * K * 256) return run(integral_constant<int, 4 * K>{}, integral_constant<int, 1>{}, T256{});
-  return run(integral_constant<int, 8 * K>{}, integral_constant<int, 1>{}, T1024{});
+  // two 16-byte vectors of a row a thread (eight single elements); the longest rows more
+  constexpr int K = E == 1 ? 8 : 2;
+  if (vecs <= K * 256) return run(integral_constant<int, K>{}, integral_constant<int, 256>{});
+  if (vecs <= K * 512) return run(integral_constant<int, K>{}, integral_constant<int, 512>{});
+  return run(integral_constant<int, E == 1 ? 32 : 10>{}, integral_constant<int, 512>{});
 }
 
 }  // namespace

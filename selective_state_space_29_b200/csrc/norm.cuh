@@ -6,17 +6,18 @@
 //     dweight = sum over rows of dy xh,  dbias = sum over rows of dy
 //
 // Both directions are bound by HBM: 4 bytes an element forward and 6 backward
-// (bf16), each read once.  A thread takes VPT vectors of channels through RT
-// rows, all of them loaded into registers, as they are, before anything else:
-// weight and bias, and the sums of their gradients, are then shared by RT rows
-// (with a row to a warp they are read again for every row, and cost L1 twice
-// the row's own bytes), and so are the meetings of a row's warps.  The RT rows'
-// sums go over the lanes together: each exchange halves the number of sums a
-// lane holds, 7 exchanges for 8 sums in place of 40.
-//   forward:  one CTA to a few rows, many CTAs to an SM.
-//   backward: CTAs walk the rows, hold the next ones while they work on these,
-//             and keep the sums of the weight's and bias' gradients in
-//             registers; a second kernel joins the CTAs' sums in order.
+// (bf16), each read once.
+//   forward:  a thread takes VPT vectors of channels through RT rows, all of
+//             them loaded into registers, as they are, before anything else.
+//             Weight and bias are then read once for RT rows (with a row to a
+//             warp they cost L1 twice the row's own bytes), and a row's warps
+//             meet once for RT rows.  The RT rows' sums go over the lanes
+//             together: each exchange halves the number of sums a lane holds.
+//             Many CTAs to an SM keep loads on their way.
+//   backward: CTAs walk the rows, and load the next ones while they work on
+//             these.  A thread has the same channels in every row, and keeps
+//             the sums of the weight's and bias' gradients in registers; a
+//             second kernel joins the CTAs' sums in order.
 // Vectors are 16 bytes.  SHIFT: rows that are not 16-byte aligned are covered by
 // aligned vectors that start up to E - 1 elements before them, the ones at a
 // row's ends by elements; a CTA's rows are a multiple of E apart, so that all
@@ -65,6 +66,7 @@ __device__ __forceinline__ float norm_rstd(float var) {
 // Where a thread stands: its vectors of E elements, and the first of its rows
 template <int E, bool SHIFT>
 struct NormPlace {
+  static constexpr bool kShift = SHIFT;
   int group, own, lanes, channels, shift;
   int64_t row;
   __device__ __forceinline__ NormPlace(const NormArgs& p, int rt) {
@@ -82,6 +84,9 @@ struct NormPlace {
   __device__ __forceinline__ bool whole(int c) const { return !SHIFT || (c >= 0 && c + E <= channels); }
   __device__ __forceinline__ bool in(int c) const { return !SHIFT || (c >= 0 && c < channels); }  // one of any()
 };
+
+template <typename Place>
+constexpr bool SHIFTED = Place::kShift;
 
 // E elements of TIO (16 bytes, or one), as they are in memory
 template <typename TIO, int E>
@@ -102,16 +107,19 @@ struct NormVec {
     if constexpr (sizeof(TIO) == 4) return __float_as_uint(__ldg(p));
     else return __ldg(reinterpret_cast<const unsigned short*>(p));
   }
+  // The vector at p, channels c.. of a row.  Elements outside the row are those
+  // of its neighbours (see trim); at the tensor's ends only the row's are read.
   template <typename Place>
-  __device__ __forceinline__ void load(const Place& at, int c, const TIO* p) {
+  __device__ __forceinline__ void load(const Place& at, int c, const TIO* p, const TIO* begin, const TIO* end) {
     if constexpr (E == 1) {
       w[0] = sizeof(TIO) == 4 ? raw(p) : raw(p) << 16;
-    } else if (at.whole(c)) {
+    } else if (!SHIFTED<Place> || (p >= begin && p + E <= end)) {
       // read once: kept out of L1, which holds weight and bias
       asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                    : "l"(p));
     } else {
+      zero();
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (at.in(c + e)) {
@@ -119,6 +127,17 @@ struct NormVec {
           else w[e / 2] |= raw(p + e) << (16 * (e & 1));
         }
     }
+  }
+  // zeros for the elements outside the row
+  template <typename Place>
+  __device__ __forceinline__ void trim(const Place& at, int c) {
+    if (at.whole(c)) return;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (!at.in(c + e)) {
+        if constexpr (sizeof(TIO) == 4) w[e] = 0u;
+        else w[e / 2] &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
+      }
   }
   // as pairs of floats (one element: y = 0)
   __device__ __forceinline__ void get(float2 (&v)[kP]) const {
@@ -224,15 +243,25 @@ template <typename TIO, int E, int VPT, int RT, bool SHIFT>
 struct NormTile {
   using Place = NormPlace<E, SHIFT>;
   NormVec<TIO, E> v[RT][VPT];
-  __device__ __forceinline__ void load(const Place& at, const TIO* from, int pitch, int live) {
+  __device__ __forceinline__ void load(const Place& at, const TIO* from, int pitch, int live, const TIO* begin,
+                                       const TIO* end) {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         v[i][j].zero();
         const int c = at.first(j);
-        if (i < live && at.any(c)) v[i][j].load(at, c, from + i * pitch + j * at.lanes * E);
+        if (i < live && at.any(c)) v[i][j].load(at, c, from + i * pitch + j * at.lanes * E, begin, end);
       }
+    trim(at);
+  }
+  __device__ __forceinline__ void trim(const Place& at) {
+    if (SHIFT) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) v[i][j].trim(at, at.first(j));
+    }
   }
   __device__ __forceinline__ void again() {
 #pragma unroll
@@ -260,7 +289,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) norm_kernel(c
   griddep_launch_dependents();
   griddep_wait();
   NormTile<TIO, E, VPT, RT, SHIFT> x;
-  x.load(at, static_cast<const TIO*>(p.x) + first, pitch, live);
+  const TIO* begin = static_cast<const TIO*>(p.x);
+  x.load(at, begin + first, pitch, live, begin, begin + p.rows * p.channels);
   float mean[RT], rstd[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) mean[i] = 0.0f;
@@ -337,117 +367,113 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) norm_kernel(c
   }
 }
 
-#ifndef NB_AHEAD
-#define NB_AHEAD 0
-#endif
-#ifndef NB_MIN
-#define NB_MIN 2
-#endif
-template <typename TIO, int E, int VPT, int RT, bool SHIFT, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 && VPT * E <= 8 ? NB_MIN : 1)
-norm_backward_kernel(const NormArgs p) {
+// Sums of two values over a row's lanes, in every one of them.  A row's warps
+// meet at a barrier of their own; calls take turns with two sets of `part`.
+__device__ __forceinline__ void norm_pair_sum(float (&v)[2], int lanes, int group, float2* part) {
+  if (lanes >= 32) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+      v[1] += __shfl_xor_sync(0xffffffffu, v[1], o);
+    }
+  } else {
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+      v[1] += __shfl_xor_sync(0xffffffffu, v[1], o);
+    }
+  }
+  if (lanes > 32) {
+    const int warps = lanes >> 5;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(v[0], v[1]);
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(lanes) : "memory");
+    part += group * warps;
+    v[0] = v[1] = 0.0f;
+#pragma unroll 4
+    for (int w = 0; w < warps; ++w) {
+      const float2 f = part[w];
+      v[0] += f.x;
+      v[1] += f.y;
+    }
+  }
+}
+
+// One row at a time to a group of threads (several rows at once need more
+// registers than they save instructions here: 16384 x 2048 bf16 took 51 us so,
+// 44 this way), the next one already on its way.
+template <typename TIO, int E, int VPT, bool SHIFT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward_kernel(const NormArgs p) {
   using Vec = NormVec<TIO, E>;
-  using Tile = NormTile<TIO, E, VPT, RT, SHIFT>;
+  using Tile = NormTile<TIO, E, VPT, 1, SHIFT>;
   constexpr int P = Vec::kP;
-  constexpr bool kAhead = NB_AHEAD;
+  constexpr bool kHold = VPT * E <= 16;  // the weight in registers
   extern __shared__ __align__(16) float norm_smem[];
-  __shared__ float part[2][32 * 2 * RT], total[2][32 * 2 * RT];
-  const NormPlace<E, SHIFT> at(p, RT);
+  __shared__ float2 part[2][THREADS / 32];
+  const NormPlace<E, SHIFT> at(p, 1);
   const float n = (float)p.channels, rcp_n = 1.0f / n;
   const bool wide = !SHIFT && ((uintptr_t)p.weight & 15) == 0;
-  const int pitch = p.period * p.channels;
   griddep_launch_dependents();
   griddep_wait();
-  float2 dw[VPT][P], db[VPT][P];
+  float2 w[VPT][P], dw[VPT][P], db[VPT][P];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j)
+  for (int j = 0; j < VPT; ++j) {
+    if (kHold && at.any(at.first(j))) Vec::param(at, p.weight, at.first(j), wide, 1.0f, w[j]);
 #pragma unroll
     for (int k = 0; k < P; ++k) dw[j][k] = db[j][k] = pair_of(0.0f);
+  }
   const int64_t first = at.row * p.channels + at.first(0);
-  const TIO* from_x = static_cast<const TIO*>(p.x) + first;
-  const TIO* from_g = static_cast<const TIO*>(p.dy) + first;
+  const int64_t step = (int64_t)(gridDim.x / p.period) * p.period * p.groups, stride = step * p.channels;
+  const TIO *begin_x = static_cast<const TIO*>(p.x), *end_x = begin_x + p.rows * p.channels, *x = begin_x + first;
+  const TIO *begin_g = static_cast<const TIO*>(p.dy), *end_g = begin_g + p.rows * p.channels, *g = begin_g + first;
   TIO* dx = static_cast<TIO*>(p.y) + first;
-  Tile ahead_x, ahead_g;
-  float ahead_mean[RT], ahead_rstd[RT];
-  auto load = [&](int64_t row, int live) {
-    ahead_x.load(at, from_x, pitch, live);
-    ahead_g.load(at, from_g, pitch, live);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      ahead_mean[i] = i < live && !p.rms ? __ldg(p.mean_in + row + i * p.period) : 0.0f;
-      ahead_rstd[i] = i < live ? __ldg(p.rstd_in + row + i * p.period) : 0.0f;  // 0: no row adds nothing
-    }
-  };
-  const int64_t step = (int64_t)(gridDim.x / p.period) * p.period * p.groups * RT, stride = step * p.channels;
+  Tile next_x, next_g;
+  float next_mean, next_rstd;
   int64_t row = at.row;
-  int live = norm_live(p, row, RT), turn = 0;
-  if (kAhead) load(row, live);
+  auto load = [&](int64_t r) {
+    const bool live = r < p.rows;
+    next_x.load(at, x, 0, live, begin_x, end_x);
+    next_g.load(at, g, 0, live, begin_g, end_g);
+    next_mean = live && !p.rms ? __ldg(p.mean_in + r) : 0.0f;
+    next_rstd = live ? __ldg(p.rstd_in + r) : 0.0f;
+    x += stride;
+    g += stride;
+  };
+  load(row);
+  int turn = 0;
   // by the CTA's first row, so that its threads stay together
-  for (int64_t r0 = row - (int64_t)at.group * RT * p.period; r0 < p.rows; r0 += step, turn ^= 1) {
-    if (!kAhead) load(row, live);
-    Tile x = ahead_x, g = ahead_g;
-    float mean[RT], rstd[RT], s[2 * RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) mean[i] = ahead_mean[i], rstd[i] = ahead_rstd[i];
-    const int now = live;
-    row += step;
-    from_x += stride;
-    from_g += stride;
-    live = norm_live(p, row, RT);
-    if (kAhead) load(row, live);
-    float2 s1[RT], s2[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) s1[i] = s2[i] = pair_of(0.0f);
+  for (int64_t r0 = row - (int64_t)at.group * p.period; r0 < p.rows; r0 += step, row += step, turn ^= 1) {
+    const float mean = next_mean, rstd = next_rstd;
+    float2 xh[VPT][P], d[VPT][P], s1 = pair_of(0.0f), s2 = pair_of(0.0f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = at.first(j);
+      float2 gy[P];
+      next_x.v[0][j].get(xh[j]);
+      next_g.v[0][j].get(gy);  // 0 outside the row, where nothing is added then
       if (!at.any(c)) continue;
-      float2 w[P];
-      Vec::param(at, p.weight, c, wide, 1.0f, w);
+      if (!kHold) Vec::param(at, p.weight, c, wide, 1.0f, w[j]);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        float2 fx[P], fg[P];
-        x.v[i][j].get(fx);
-        g.v[i][j].get(fg);  // 0 outside the row, where nothing is added then
-#pragma unroll
-        for (int k = 0; k < P; ++k) {
-          const float2 xh = __fmul2_rn(__fadd2_rn(fx[k], pair_of(-mean[i])), pair_of(rstd[i]));
-          const float2 d = __fmul2_rn(fg[k], w[k]);
-          s1[i] = __fadd2_rn(s1[i], d);
-          s2[i] = __ffma2_rn(d, xh, s2[i]);
-          dw[j][k] = __ffma2_rn(fg[k], xh, dw[j][k]);
-          db[j][k] = __fadd2_rn(db[j][k], fg[k]);
-        }
+      for (int k = 0; k < P; ++k) {
+        xh[j][k] = __fmul2_rn(__fadd2_rn(xh[j][k], pair_of(-mean)), pair_of(rstd));
+        d[j][k] = __fmul2_rn(gy[k], w[j][k]);
+        s1 = __fadd2_rn(s1, d[j][k]);
+        s2 = __ffma2_rn(d[j][k], xh[j][k], s2);
+        dw[j][k] = __ffma2_rn(gy[k], xh[j][k], dw[j][k]);
+        db[j][k] = __fadd2_rn(db[j][k], gy[k]);
       }
     }
+    load(row + step);
+    float s[2] = {E == 1 ? s1.x : s1.x + s1.y, E == 1 ? s2.x : s2.x + s2.y};
+    norm_pair_sum(s, p.lanes, at.group, part[turn]);
+    const float a1 = p.rms ? 0.0f : over(s[0], n, rcp_n), a2 = over(s[1], n, rcp_n);
+    if (row < p.rows) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      s[i] = E == 1 ? s1[i].x : s1[i].x + s1[i].y;
-      s[RT + i] = E == 1 ? s2[i].x : s2[i].x + s2[i].y;
-    }
-    x.again();
-    g.again();
-    norm_total(s, p.lanes, at.group, p.groups, part[turn], total[turn],
-               [&](int i, float t) { return p.rms && i < RT ? 0.0f : over(t, n, rcp_n); });
+      for (int j = 0; j < VPT; ++j) {
+        const int c = at.first(j);
+        if (!at.any(c)) continue;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int c = at.first(j);
-      if (!at.any(c)) continue;
-      float2 w[P];
-      Vec::param(at, p.weight, c, wide, 1.0f, w);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        if (i >= now) continue;
-        float2 fx[P], fg[P];
-        x.v[i][j].get(fx);
-        g.v[i][j].get(fg);
-#pragma unroll
-        for (int k = 0; k < P; ++k) {
-          const float2 xh = __fmul2_rn(__fadd2_rn(fx[k], pair_of(-mean[i])), pair_of(rstd[i]));
-          fx[k] = __fmul2_rn(__ffma2_rn(xh, pair_of(-s[RT + i]), __ffma2_rn(fg[k], w[k], pair_of(-s[i]))),
-                             pair_of(rstd[i]));
-        }
-        Vec::put(at, c, dx + i * pitch + j * at.lanes * E, fx);
+        for (int k = 0; k < P; ++k)
+          d[j][k] = __fmul2_rn(__ffma2_rn(xh[j][k], pair_of(-a2), __fadd2_rn(d[j][k], pair_of(-a1))), pair_of(rstd));
+        Vec::put(at, c, dx + j * at.lanes * E, d[j]);
       }
     }
     dx += stride;
