@@ -485,21 +485,23 @@ def state_update_mimo(state, x, delta, A, B, C, D=None, y=None, stream=None):
 
 
 # --- gated recurrence and layer norm ------------------------------------------------
+# These calls take microseconds on the GPU for one token, so their host side is
+# kept short: the entry point is called directly, and the current stream's
+# handle is taken without a Stream object.
 
 def _current_stream_handle(index):
-    """The current stream's handle on device `index` (without the Stream
-    object that torch.cuda.current_stream makes, 3 us of a 10 us call)."""
+    """The current stream's handle on device `index` (torch.cuda.current_stream
+    makes a Stream object: 3 us of a 10 us call)."""
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return torch.cuda.current_stream(index).cuda_stream if raw is None else raw(index)
 
 
-def _on_stream(x, stream, inputs, call):
-    """call(handle) -> tensors it allocated, made with x's device current and
-    on `stream` (None: that device's current stream).  On another stream than
+def _on_stream(device, stream, inputs, call):
+    """call(handle) -> tensors it allocated, made with `device` current and on
+    `stream` (None: that device's current stream).  On another stream than
     the current one, inputs and results are marked as used on both."""
     import torch
-    device = x.device
     if stream is None and device.index == torch.cuda.current_device():
         return call(_current_stream_handle(device.index))
     with torch.cuda.device(device):
@@ -538,7 +540,16 @@ def _expect_cuda(name, t, dims):
                          f"{t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-_GATE_FLAGS = {"sigmoid": 0, "log": MAMBA_GATE_LOG}
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+_GATE_FLAGS = {("sigmoid", False): 0, ("log", False): MAMBA_GATE_LOG, ("sigmoid", True): MAMBA_GATE_CONVEX,
+               ("log", True): MAMBA_GATE_LOG | MAMBA_GATE_CONVEX}
+
+
+def _blocks(length):
+    return -(-length // MAMBA_GATED_SCAN_BLOCK)
 
 
 def gated_scan(x, gate, initial_state=None, return_final_state=True, gate_form="sigmoid", convex=False,
@@ -552,17 +563,16 @@ def gated_scan(x, gate, initial_state=None, return_final_state=True, gate_form="
     receives the states gated_scan_backward can start from."""
     import torch
     _expect_cuda("x", x, 3)
-    shape, dtype, device = x.shape, x.dtype, x.device
+    shape, dtype, device, f32 = x.shape, x.dtype, x.device, torch.float32
     code = dtype_code(dtype)
     batch, length, channels = shape
     rows = (batch, channels)
-    flags = _GATE_FLAGS[gate_form] | (MAMBA_GATE_CONVEX if convex else 0)
-    f32 = torch.float32
+    flags = _GATE_FLAGS[gate_form, bool(convex)]
     _expect("gate", gate, shape, dtype, device)
     if initial_state is not None:
         _expect("initial_state", initial_state, rows, f32, device)
     if checkpoints is not None:
-        _expect("checkpoints", checkpoints, (batch, -(-length // MAMBA_GATED_SCAN_BLOCK), channels), f32, device)
+        _expect("checkpoints", checkpoints, (batch, _blocks(length), channels), f32, device)
     if y is not None:
         _expect("y", y, shape, dtype, device)
     if final_state is not None:
@@ -573,17 +583,18 @@ def gated_scan(x, gate, initial_state=None, return_final_state=True, gate_form="
         last = final_state
         if last is None and return_final_state:
             last = x.new_empty(rows, dtype=f32)
-        mamba_gated_scan(x, gate, initial_state, out, last, checkpoints, batch, length, channels, flags, code, handle)
+        _check(library().mamba_gated_scan(x.data_ptr(), gate.data_ptr(), _at(initial_state), out.data_ptr(), _at(last),
+                                          _at(checkpoints), batch, length, channels, flags, code, handle),
+               "mamba_gated_scan")
         return out, last
-    return _on_stream(x, stream, (x, gate, initial_state, checkpoints), call)
+    return _on_stream(device, stream, (x, gate, initial_state, checkpoints), call)
 
 
 def gated_scan_checkpoints(x):
     """An empty float32 (batch, blocks, channels) tensor for gated_scan's checkpoints."""
     import torch
     _expect_cuda("x", x, 3)
-    return torch.empty((x.shape[0], -(-x.shape[1] // MAMBA_GATED_SCAN_BLOCK), x.shape[2]), device=x.device,
-                       dtype=torch.float32)
+    return x.new_empty((x.shape[0], _blocks(x.shape[1]), x.shape[2]), dtype=torch.float32)
 
 
 def gated_scan_backward(x, gate, dy, initial_state=None, d_final_state=None, checkpoints=None, gate_form="sigmoid",
@@ -594,12 +605,11 @@ def gated_scan_backward(x, gate, dy, initial_state=None, d_final_state=None, che
     Returns a dict: dx, dgate (dtype of x), d_initial_state (float32)."""
     import torch
     _expect_cuda("x", x, 3)
-    shape, dtype, device = x.shape, x.dtype, x.device
+    shape, dtype, device, f32 = x.shape, x.dtype, x.device, torch.float32
     code = dtype_code(dtype)
     batch, length, channels = shape
     rows = (batch, channels)
-    flags = _GATE_FLAGS[gate_form] | (MAMBA_GATE_CONVEX if convex else 0)
-    f32 = torch.float32
+    flags = _GATE_FLAGS[gate_form, bool(convex)]
     _expect("gate", gate, shape, dtype, device)
     _expect("dy", dy, shape, dtype, device)
     if initial_state is not None:
@@ -607,15 +617,17 @@ def gated_scan_backward(x, gate, dy, initial_state=None, d_final_state=None, che
     if d_final_state is not None:
         _expect("d_final_state", d_final_state, rows, f32, device)
     if checkpoints is not None:
-        _expect("checkpoints", checkpoints, (batch, -(-length // MAMBA_GATED_SCAN_BLOCK), channels), f32, device)
+        _expect("checkpoints", checkpoints, (batch, _blocks(length), channels), f32, device)
 
     def call(handle):
         dx, dgate = torch.empty_like(x), torch.empty_like(gate)
         dh = x.new_empty(rows, dtype=f32)
-        mamba_gated_scan_backward(x, gate, initial_state, checkpoints, dy, d_final_state, dx, dgate, dh, batch,
-                                  length, channels, flags, code, handle)
+        _check(library().mamba_gated_scan_backward(
+            x.data_ptr(), gate.data_ptr(), _at(initial_state), _at(checkpoints), dy.data_ptr(), _at(d_final_state),
+            dx.data_ptr(), dgate.data_ptr(), dh.data_ptr(), batch, length, channels, flags, code, handle),
+            "mamba_gated_scan_backward")
         return dx, dgate, dh
-    dx, dgate, dh = _on_stream(x, stream, (x, gate, dy, initial_state, d_final_state, checkpoints), call)
+    dx, dgate, dh = _on_stream(device, stream, (x, gate, dy, initial_state, d_final_state, checkpoints), call)
     return {"dx": dx, "dgate": dgate, "d_initial_state": dh}
 
 
@@ -630,22 +642,24 @@ def gated_step(state, x, gate, gate_form="sigmoid", convex=False, y=None, stream
     _expect("state", state, shape, torch.float32, device)
     if y is not None:
         _expect("y", y, shape, dtype, device)
-    flags = _GATE_FLAGS[gate_form] | (MAMBA_GATE_CONVEX if convex else 0)
+    flags = _GATE_FLAGS[gate_form, bool(convex)]
 
     def call(handle):
         out = torch.empty_like(x) if y is None else y
-        mamba_gated_step(state, x, gate, out, shape[0], shape[1], flags, code, handle)
+        _check(library().mamba_gated_step(state.data_ptr(), x.data_ptr(), gate.data_ptr(), out.data_ptr(), shape[0],
+                                          shape[1], flags, code, handle), "mamba_gated_step")
         return (out,)
-    return _on_stream(x, stream, (x, gate, state), call)[0]
+    return _on_stream(device, stream, (x, gate, state), call)[0]
 
 
 def _norm_rows(x):
     if x.dim() == 0 or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"x: expected a contiguous CUDA tensor of rows, got {tuple(x.shape)} on {x.device}")
+    shape = x.shape
     rows = 1
-    for n in x.shape[:-1]:
+    for n in shape[:-1]:
         rows *= n
-    return rows, x.shape[-1]
+    return shape[:-1], rows, shape[-1]
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, y=None, stream=None):
@@ -655,24 +669,25 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, y=None, stream=No
     no mean is taken off (mean is then zero).  mean, rstd: x.shape[:-1]
     float32, for layer_norm_backward."""
     import torch
-    rows, channels = _norm_rows(x)
-    dtype, device = x.dtype, x.device
+    outer, rows, channels = _norm_rows(x)
+    dtype, device, f32 = x.dtype, x.device, torch.float32
     code = dtype_code(dtype)
-    f32 = torch.float32
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _expect(name, t, (channels,), f32, device)
+    if weight is not None:
+        _expect("weight", weight, (channels,), f32, device)
+    if bias is not None:
+        _expect("bias", bias, (channels,), f32, device)
     if y is not None:
         _expect("y", y, x.shape, dtype, device)
 
     def call(handle):
         out = torch.empty_like(x) if y is None else y
-        mean = x.new_empty(x.shape[:-1], dtype=f32)
+        mean = x.new_empty(outer, dtype=f32)
         rstd = torch.empty_like(mean)
-        mamba_layer_norm(x, weight, bias, out, mean, rstd, rows, channels, eps, MAMBA_NORM_RMS if rms else 0, code,
-                         handle)
+        _check(library().mamba_layer_norm(x.data_ptr(), _at(weight), _at(bias), out.data_ptr(), mean.data_ptr(),
+                                          rstd.data_ptr(), rows, channels, eps, MAMBA_NORM_RMS if rms else 0, code,
+                                          handle), "mamba_layer_norm")
         return out, mean, rstd
-    return _on_stream(x, stream, (x, weight, bias), call)
+    return _on_stream(device, stream, (x, weight, bias), call)
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, rms=False, stream=None):
@@ -680,23 +695,23 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias=True, rms=False, stream=
     rstd the forward call returned.  Returns a dict: dx (dtype of x), dweight
     (None without a weight), dbias (None with bias=False), float32."""
     import torch
-    rows, channels = _norm_rows(x)
-    dtype, device = x.dtype, x.device
+    outer, rows, channels = _norm_rows(x)
+    dtype, device, f32 = x.dtype, x.device, torch.float32
     code = dtype_code(dtype)
-    f32 = torch.float32
     _expect("dy", dy, x.shape, dtype, device)
     if weight is not None:
         _expect("weight", weight, (channels,), f32, device)
     if mean is not None or not rms:
-        _expect("mean", mean, x.shape[:-1], f32, device)
-    _expect("rstd", rstd, x.shape[:-1], f32, device)
+        _expect("mean", mean, outer, f32, device)
+    _expect("rstd", rstd, outer, f32, device)
 
     def call(handle):
         dx = torch.empty_like(x)
         dw = None if weight is None else torch.empty_like(weight)
-        db = x.new_empty((channels,), dtype=f32) if bias else None
-        mamba_layer_norm_backward(dy, x, weight, mean, rstd, dx, dw, db, rows, channels,
-                                  MAMBA_NORM_RMS if rms else 0, code, handle)
+        db = None if not bias else x.new_empty((channels,), dtype=f32) if dw is None else torch.empty_like(dw)
+        _check(library().mamba_layer_norm_backward(
+            dy.data_ptr(), x.data_ptr(), _at(weight), _at(mean), rstd.data_ptr(), dx.data_ptr(), _at(dw), _at(db), rows,
+            channels, MAMBA_NORM_RMS if rms else 0, code, handle), "mamba_layer_norm_backward")
         return dx, dw, db
-    dx, dw, db = _on_stream(x, stream, (dy, x, weight, mean, rstd), call)
+    dx, dw, db = _on_stream(device, stream, (dy, x, weight, mean, rstd), call)
     return {"dx": dx, "dweight": dw, "dbias": db}
