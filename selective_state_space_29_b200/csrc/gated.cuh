@@ -67,6 +67,7 @@ struct GatedArgs {
   void* dgate;
   float* dh0;
   unsigned long long* rec;  // [blocks][chains][channels of a tile] records, all bits set
+  int* ticket;           // tiles handed out, starting at -1; NULL: dealt by block index
   int64_t len, channels;
   int blocks;            // tiles along time
   int groups;            // channel groups
@@ -354,6 +355,25 @@ struct GatedBars {
   uint64_t full[kGatedStages], mapped[2], entered[2], freed[2], placed[2];
 };
 
+// The next tile of a CTA: the counter's, or the next of its own.  ask() does not
+// wait for the counter's answer, get() does.
+struct GatedNext {
+  int raw, job;  // job: that of the tile before, then the answer
+  __device__ __forceinline__ void ask(const GatedArgs& p) {
+    raw = 0;
+    const unsigned counted = p.ticket && job < p.jobs && (threadIdx.x & 31) == 0;
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+                 "@q atom.relaxed.gpu.global.add.s32 %0, [%1], 1;\n\t}"
+                 : "+r"(raw) : "l"(p.ticket), "r"(counted) : "memory");
+  }
+  __device__ __forceinline__ int get(const GatedArgs& p) {
+    if (job >= p.jobs) job = p.jobs;
+    else if (p.ticket) job = __shfl_sync(0xffffffffu, raw, 0) + 1;
+    else job = job < 0 ? (int)blockIdx.x : min(job + (int)gridDim.x, p.jobs);
+    return job;
+  }
+};
+
 // Waits end: everything waited for is bounded itself.  Once an error is on
 // record nobody waits long.
 __device__ __forceinline__ uint64_t gated_limit(const GatedArgs& p) {
@@ -456,19 +476,21 @@ struct GatedLoader {
     }
   }
   __device__ __forceinline__ void run() {
-    int job = blockIdx.x;
+    GatedNext next;
+    next.job = -1;
 #pragma unroll
-    for (int s = 0; s < kGatedStages; ++s, job = min(job + (int)gridDim.x, p.jobs)) {
-      const GatedTile t = place(s, job);
+    for (int s = 0; s < kGatedStages; ++s) {
+      next.ask(p);
+      const GatedTile t = place(s, next.get(p));
       if (CB < 16 && (threadIdx.x & 31) == 0) mbar_arrive(&bars->placed[s]);
       load(s, t);
     }
     // after the tile that ends the CTA nothing is left to place
     for (int it = 0; reinterpret_cast<const GatedTile*>(smem + SM::kTiles)[it & 3].job < p.jobs; ++it) {
       const int par = it & 1;
+      next.ask(p);
       gated_wait(p, BACKWARD ? &bars->freed[par] : &bars->mapped[par], (it >> 1) & 1);
-      const GatedTile t = place(it + 2, job);
-      job = min(job + (int)gridDim.x, p.jobs);
+      const GatedTile t = place(it + 2, next.get(p));
       if (CB < 16 && (threadIdx.x & 31) == 0) mbar_arrive(&bars->placed[par]);
       load(it + 2, t);
     }
@@ -839,6 +861,14 @@ gated_backward_kernel(const GatedArgs p, const __grid_constant__ CUtensorMap map
       load(it + kGatedStages);
     }
   }
+}
+
+// Records not yet written, and the counter before the first tile
+__global__ void __launch_bounds__(256) gated_clear_kernel(uint4* p, int64_t n) {
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
 // One token per sequence, state in place.
