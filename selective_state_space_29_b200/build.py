@@ -26,7 +26,6 @@ NVCC_FLAGS = [
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC,-O2",
     "-Xptxas", "-v",
-    "-split-compile=0",
     "-cudart", "static",
     "-shared",
 ]

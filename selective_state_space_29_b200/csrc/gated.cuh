@@ -51,7 +51,7 @@ constexpr int kGatedTok = kGatedBlock / kGatedSegs;  // tokens of a segment
 constexpr int kGatedRow = 64;                        // bytes of a token's channels in a tile
 constexpr int kGatedSegBytes = kGatedTok * kGatedRow;
 constexpr int kGatedStream = kGatedSegs * kGatedSegBytes;  // bytes of one tensor's tile
-constexpr int kGatedWindow = 8;                      // records looked at together
+constexpr int kGatedWindow = 16;                     // records looked at together, at most
 static_assert(kGatedWorkers == kGatedSegs * 16, "16 lanes per segment");
 
 struct GatedArgs {
@@ -75,6 +75,7 @@ struct GatedArgs {
   int jobs;              // chains * blocks
   unsigned rcp_chains, rcp_groups;  // floor(2^32 / ...), for divisions
   int box;               // tokens of a TMA box
+  int look;              // records looked at together: the tiles of a chain that are worked on at a time, and some
   uint64_t wait_limit_ns;
 };
 
@@ -265,28 +266,40 @@ __device__ __forceinline__ unsigned long long rec_get(const unsigned long long* 
 // lane is done.
 struct GatedLook {
   unsigned long long r[kGatedWindow];
-  __device__ __forceinline__ void ask(const unsigned long long* own, int before, int64_t stride, bool done) {
+  __device__ __forceinline__ void ask(const unsigned long long* own, int before, int64_t stride, bool done, int look) {
 #pragma unroll
-    for (int i = 0; i < kGatedWindow; ++i) {
-      r[i] = ~0ull;
-      if (!done && i < before) r[i] = rec_get(own - (i + 1) * stride);
+    for (int c = 0; c < kGatedWindow; c += 2) {
+      if (c >= look) break;  // the rest is not looked at
+#pragma unroll
+      for (int i = c; i < c + 2; ++i) {
+        r[i] = ~0ull;
+        if (!done && i < before) r[i] = rec_get(own - (i + 1) * stride);
+      }
     }
   }
-  __device__ __forceinline__ bool found(bool& done, float& h) {
+  __device__ __forceinline__ bool found(bool& done, float& h, int look) {
     int at = -1;
     bool ready = !done;
 #pragma unroll
-    for (int i = 0; i < kGatedWindow; ++i) {
-      const uint32_t pb = (uint32_t)(r[i] >> 32);
-      ready = ready && pb != 0xffffffffu;
-      if (ready && at < 0 && __uint_as_float(pb) == 0.0f) at = i;
+    for (int c = 0; c < kGatedWindow; c += 2) {
+      if (c >= look) break;
+#pragma unroll
+      for (int i = c; i < c + 2; ++i) {
+        const uint32_t pb = (uint32_t)(r[i] >> 32);
+        ready = ready && pb != 0xffffffffu;
+        if (ready && at < 0 && __uint_as_float(pb) == 0.0f) at = i;
+      }
     }
     if (at >= 0) {
       done = true;
       h = 0.0f;
 #pragma unroll
-      for (int i = kGatedWindow - 1; i >= 0; --i)
-        if (i <= at) h = fmaf(__uint_as_float((uint32_t)(r[i] >> 32)), h, __uint_as_float((uint32_t)r[i]));
+      for (int c = kGatedWindow - 2; c >= 0; c -= 2) {
+        if (c >= look) continue;
+#pragma unroll
+        for (int i = c + 1; i >= c; --i)
+          if (i <= at) h = fmaf(__uint_as_float((uint32_t)(r[i] >> 32)), h, __uint_as_float((uint32_t)r[i]));
+      }
     }
     return __all_sync(0xffffffffu, done);
   }
@@ -347,10 +360,17 @@ struct GatedSmem {
 
 // Barriers between the workers (w), the carrier (c) and the loader (l).  full,
 // l to w and c: a stage is loaded (backward, with the states that enter);
-// mapped, w to c and l: every warp's maps are written (and, forward, its stage
-// is read); entered, c to w: what enters the tile is written; freed, w to w and
-// l: backward, the stage is read to the end; placed, l to w: without TMA, the
-// tile that the workers are to load is known.
+// mapped, w and c to w, c and l: every warp's maps are written (and, forward,
+// its stage is read), and c knows the tile; entered, c to w: what enters the
+// tile is written; freed, w and c to w and l: backward, the stage and the maps
+// are read to the end; placed, l to w: without TMA, the tile that the workers
+// are to load is known.
+// A waiter tells a phase from the next but one by nothing, so a barrier's next
+// phase must not end before everyone has seen this one: full's is armed behind
+// mapped (forward) or freed, to which w and c come after they have seen it;
+// mapped's needs w and c themselves, and the stage that l loads; entered's comes
+// from c behind the next tile's mapped; freed's needs w, and l's stage;
+// placed's comes behind the tile it placed.
 struct GatedBars {
   uint64_t full[kGatedStages], mapped[2], entered[2], freed[2], placed[2];
 };
@@ -383,6 +403,11 @@ __device__ __forceinline__ void gated_wait(const GatedArgs& p, uint64_t* bar, ui
   if (mbar_try_wait(bar, parity)) return;
   if (!mbar_wait_bounded(bar, parity, 2 * gated_limit(p))) record_device_error(MAMBA_ERR_TIMEOUT);
 }
+__device__ __forceinline__ void gated_warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ void gated_arrive_async(uint64_t* bar) {  // when this thread's cp.async are done
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -512,6 +537,7 @@ __device__ __forceinline__ void gated_carry(const GatedArgs& p, unsigned char* s
     gated_wait(p, &bars->full[par], phase);
     const GatedTile t = reinterpret_cast<const GatedTile*>(smem + SM::kTiles)[it & 3];
     if (t.job >= p.jobs) return;
+    gated_warp_arrive(&bars->mapped[par]);
     const bool active = lane < kChan && t.c0 + lane < p.channels;
     const int64_t row = (int64_t)t.b * p.channels + t.c0 + lane;
     unsigned long long* rec = p.rec + (int64_t)t.k * stride + t.chain * kChan + ch;
@@ -528,9 +554,9 @@ __device__ __forceinline__ void gated_carry(const GatedArgs& p, unsigned char* s
     bool done = !active || t.k == 0, mapped = false;
     bool known = __all_sync(0xffffffffu, done);
     while (!known && !mapped) {  // ends: the workers wait for nothing but loads
-      look.ask(rec, t.k, stride, done);
+      look.ask(rec, t.k, stride, done, p.look);
       mapped = __all_sync(0xffffffffu, mbar_test_wait(&bars->mapped[par], phase));
-      if (!mapped) known = look.found(done, h);
+      if (!mapped) known = look.found(done, h, p.look);
     }
     if (known) {
       tell();
@@ -539,12 +565,13 @@ __device__ __forceinline__ void gated_carry(const GatedArgs& p, unsigned char* s
     const float* maps = reinterpret_cast<const float*>(smem + SM::kMaps) + par % SM::kMapSets * SM::kMapSet;
     float tp, th;
     gated_fold<kChan, BACKWARD>(maps, maps + (BACKWARD ? 2 : 1) * SM::kPlane, ch, tp, th);
+    if (BACKWARD) gated_warp_arrive(&bars->freed[par]);  // the maps are read
     const bool more = active && t.k + 1 < p.blocks;
     if (!known) {
       if (more) rec_put(rec, tp, th);
       uint64_t t0 = 0;
-      for (uint32_t round = 0; !look.found(done, h); ++round) {
-        look.ask(rec, t.k, stride, done);
+      for (uint32_t round = 0; !look.found(done, h, p.look); ++round) {
+        look.ask(rec, t.k, stride, done, p.look);
         if ((round & 63u) == 63u) {
           const uint64_t now = globaltimer_ns();
           if (t0 == 0) t0 = now;
@@ -601,9 +628,9 @@ __device__ __forceinline__ bool gated_begin(const GatedArgs& p, unsigned char* s
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->full[i], (CB == 16 ? 1 : kGatedWorkers) + (BACKWARD ? 1 : 0));
-      mbar_init(&bars->mapped[i], kGatedWorkers / 32);
+      mbar_init(&bars->mapped[i], kGatedWorkers / 32 + 1);
       mbar_init(&bars->entered[i], 1);
-      mbar_init(&bars->freed[i], kGatedWorkers / 32);
+      mbar_init(&bars->freed[i], kGatedWorkers / 32 + 1);
       mbar_init(&bars->placed[i], 1);
     }
     fence_mbar_init();
@@ -622,11 +649,6 @@ __device__ __forceinline__ bool gated_begin(const GatedArgs& p, unsigned char* s
 #pragma unroll
   for (int s = 0; s < kGatedStages; ++s) gated_worker_load<TIO, BACKWARD, CB>(p, smem, s);
   return true;
-}
-
-__device__ __forceinline__ void gated_warp_arrive(uint64_t* bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // ---------------------------------------------------------------------------
@@ -871,17 +893,59 @@ __global__ void __launch_bounds__(256) gated_clear_kernel(uint4* p, int64_t n) {
     p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
-// One token per sequence, state in place.
-template <typename TIO, bool LOG, bool CONVEX>
-__global__ void gated_step_kernel(float* state, const TIO* x, const TIO* gate, TIO* y, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  float2 a, w;
-  gate_decay<LOG, sizeof(TIO) == 2>(both(to_f32(gate[i])), a, w);
-  const float in = to_f32(x[i]);
-  const float h = fmaf(a.x, state[i], CONVEX ? w.x * in : in);
-  state[i] = h;
-  y[i] = from_f32<TIO>(h);
+// One token per sequence, state in place: 14 bytes a channel (bf16) and no
+// reuse.  WIDE: four channels a thread (state 16-byte, the others 8- or 16-byte
+// aligned), else one.
+template <typename TIO, bool LOG, bool CONVEX, bool WIDE>
+__global__ void __launch_bounds__(256) gated_step_kernel(float* state, const TIO* x, const TIO* gate, TIO* y, int64_t n) {
+  constexpr int N = WIDE ? 4 : 1, P = (N + 1) / 2;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * N;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (at >= n) return;
+  float2 g[P], in[P], h[P];
+  if constexpr (WIDE) {
+    const float4 s = *reinterpret_cast<const float4*>(state + at);
+    h[0] = make_float2(s.x, s.y);
+    h[1] = make_float2(s.z, s.w);
+    if constexpr (sizeof(TIO) == 2) {
+      const uint2 gw = *reinterpret_cast<const uint2*>(gate + at), xw = *reinterpret_cast<const uint2*>(x + at);
+      g[0] = Lane4<TIO>::get({gw.x});
+      g[1] = Lane4<TIO>::get({gw.y});
+      in[0] = Lane4<TIO>::get({xw.x});
+      in[1] = Lane4<TIO>::get({xw.y});
+    } else {
+      const float4 gw = *reinterpret_cast<const float4*>(gate + at), xw = *reinterpret_cast<const float4*>(x + at);
+      g[0] = make_float2(gw.x, gw.y);
+      g[1] = make_float2(gw.z, gw.w);
+      in[0] = make_float2(xw.x, xw.y);
+      in[1] = make_float2(xw.z, xw.w);
+    }
+  } else {
+    g[0] = both(to_f32(gate[at]));
+    in[0] = both(to_f32(x[at]));
+    h[0] = both(state[at]);
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    float2 a, w;
+    gate_decay<LOG, sizeof(TIO) == 2>(g[i], a, w);
+    h[i] = __ffma2_rn(a, h[i], CONVEX ? __fmul2_rn(w, in[i]) : in[i]);
+  }
+  if constexpr (WIDE) {
+    *reinterpret_cast<float4*>(state + at) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    if constexpr (sizeof(TIO) == 2) {
+      uint32_t lo[1], hi[1];
+      Lane4<TIO>::put(h[0], lo);
+      Lane4<TIO>::put(h[1], hi);
+      *reinterpret_cast<uint2*>(y + at) = make_uint2(lo[0], hi[0]);
+    } else {
+      *reinterpret_cast<float4*>(y + at) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    }
+  } else {
+    state[at] = h[0].x;
+    y[at] = from_f32<TIO>(h[0].x);
+  }
 }
 
 }  // namespace mamba

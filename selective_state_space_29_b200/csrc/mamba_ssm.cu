@@ -862,13 +862,6 @@ int copy_state(float* to, const float* from, int64_t batch, int64_t channels, cu
   return e == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA;
 }
 
-template <typename... K, typename... A>
-int launch_1d(void (*kernel)(K...), int64_t blocks, int threads, cudaStream_t stream, A... a) {
-  if (blocks >= (int64_t(1) << 31)) return MAMBA_ERR_UNSUPPORTED;
-  kernel<<<(unsigned)blocks, threads, 0, stream>>>(a...);
-  return cudaGetLastError() == cudaSuccess ? MAMBA_OK : MAMBA_ERR_CUDA;
-}
-
 // One pass over every tile: the forward kernel, or the backward one
 template <typename TIO, bool LOG, bool CONVEX, bool BACKWARD, int CB>
 int launch_gated_pass(const GatedArgs& p, const CUtensorMap (&maps)[3], cudaStream_t stream) {
@@ -945,6 +938,11 @@ int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int 
   int sms = 0;
   if (int e = current_sms(&sms)) return e;
   const bool counted = blocks > 1 && p.chains >= 2 * sms;
+  // every record looked at costs, missing the one needed costs a round more
+  // (1 x 131072 x 2048 bf16, where about five tiles of a chain are worked on at
+  // a time: 347 us with 8 records, 384 with 16, 459 with 24; with 64 channels,
+  // one chain pair: 305, 199, 193)
+  p.look = std::min(kGatedWindow, 2 * sms / p.chains + 2);
   // scratch: a counter and records for every pass over several tiles of time,
   // and the checkpoints that a backward call has not been given
   const bool own_ckpt = backward && !p.ckpt;
@@ -1739,9 +1737,15 @@ int mamba_gated_step(float* state, const void* x, const void* gate, void* y, int
   if (!outputs_apart({{state, batch * channels * 4}, {y, io}}, {{x, io}, {gate, io}})) return MAMBA_ERR_INVALID_ARG;
   return dispatch_gate(dtype, flags, [&](auto tio, auto log, auto convex) -> int {
     using TIO = decltype(tio);
+    constexpr bool L = decltype(log)::value, C = decltype(convex)::value;
     const int64_t n = batch * channels;
-    return launch_1d(gated_step_kernel<TIO, decltype(log)::value, decltype(convex)::value>, (n + 255) / 256, 256, stream,
-              state, static_cast<const TIO*>(x), static_cast<const TIO*>(gate), static_cast<TIO*>(y), n);
+    const bool wide = n % 4 == 0 && aligned(state, 16) && aligned(x, 4 * es) && aligned(gate, 4 * es) && aligned(y, 4 * es);
+    auto kernel = wide ? gated_step_kernel<TIO, L, C, true> : gated_step_kernel<TIO, L, C, false>;
+    const int64_t each = wide ? 1024 : 256;
+    return launch_pdl(kernel, dim3((unsigned)((n + each - 1) / each)), dim3(256), 0, stream, state,
+                      static_cast<const TIO*>(x), static_cast<const TIO*>(gate), static_cast<TIO*>(y), n) == cudaSuccess
+               ? MAMBA_OK
+               : MAMBA_ERR_CUDA;
   });
 }
 

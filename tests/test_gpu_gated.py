@@ -314,3 +314,19 @@ def test_captured_graphs_replayed_with_new_inputs():
         again = before
         y = m.gated_step(again, new["x"][:, 0].contiguous(), new["gate"][:, 0].contiguous())
         assert torch.equal(state, again) and torch.equal(outs[2], y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 16384, 1000), (1, 9000, 2048), (8, 2048, 512), (3, 2500, 333), (40, 300, 72)])
+def test_no_wait_runs_out_over_many_calls(shape, dtype):
+    """Many calls of many tiles a CTA, the last ones among them: the warps of a
+    CTA hand barriers on without losing a phase, and every call gives the same bits."""
+    d = make(*shape, DT[dtype], "log", seed=4)
+    first = None
+    for _ in range(25):
+        y, f = m.gated_scan(d["x"], d["gate"], gate_form="log", convex=True)
+        g = m.gated_scan_backward(d["x"], d["gate"], d["dy"], gate_form="log", convex=True)
+        got = [y, f, *g.values()]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+    assert m.mamba_get_device_error() == m.MAMBA_OK
