@@ -18,11 +18,13 @@
 //     of channels.  A segment is the map h -> P h + H (P the product of its
 //     gates, H its end state from zero); a and w x stay in registers between
 //     the pass that forms the map and the pass that writes y.
-//   - Tiles are staged in shared memory by cp.async, the next ones while this
-//     one is worked on, by persistent CTAs, two per SM.
-//   - One warp, a lane per channel, joins the segments' maps, publishes the
-//     tile's map, looks back for the state that enters the tile, and hands
-//     every segment its entering state.
+//   - Tiles are staged in shared memory, the next one while this one is worked
+//     on, by persistent CTAs, two per SM: a loader warp brings them by TMA
+//     (tensors whose rows are not 16-byte aligned: the workers by cp.async of 4
+//     bytes, or by single elements).
+//   - A carrier warp, a lane per channel, looks for the state that enters the
+//     tile while the workers make the segments' maps, joins the maps, and hands
+//     on what leaves the tile.
 // Time goes across CTAs: a tile's record in global memory is one 64-bit word
 // per channel, (P, H), replaced by (0, state after the tile) once that is
 // known; a map with P = 0 does not depend on what enters, so both are read the
@@ -30,11 +32,21 @@
 // all bits set (which no (P, H) has) means not yet written.  The state that
 // enters a tile is folded from the nearest record with P = 0 onwards, in time
 // order: every tile rounds the same way whoever folds it, so results do not
-// change from call to call.  Tiles are handed out by an atomic counter in time
-// order, all chains (batch row, channel group) of a time before the next, so
-// the smallest unfinished tile is always in a running CTA and the waits end.
+// change from call to call.  Tiles go in time order, all chains (batch row,
+// channel group) of a time before the next, to CTAs that take them from a
+// counter, or that are all on the GPU at once (cooperative launch) and take every
+// nth: the smallest unfinished tile is always being worked on, so the
+// waits end.
 // The backward pass walks the tiles in reverse with the adjoint's maps, from
 // the states that enter every block of 256 tokens (checkpoints).
+//
+// Measured (B200, share of the 6.55 TB/s a copy reaches, each tensor counted
+// once): 8 x 2048 x 2048 bf16 forward 37 us (0.83), gradients with states saved
+// 62 us (0.82); float32 forward 64 us (0.95): the bf16 kernels issue twice the
+// instructions a byte, at half of the issue slots.  1 x 131072 x 2048 bf16
+// forward 344 us (0.72): five tiles of a chain are worked on at a time, and each
+// waits about 2,000 cycles for the ones before it.  What is left there is the
+// wait's length against two tiles an SM; more do not fit its registers.
 #pragma once
 
 #include <type_traits>
@@ -51,7 +63,6 @@ constexpr int kGatedTok = kGatedBlock / kGatedSegs;  // tokens of a segment
 constexpr int kGatedRow = 64;                        // bytes of a token's channels in a tile
 constexpr int kGatedSegBytes = kGatedTok * kGatedRow;
 constexpr int kGatedStream = kGatedSegs * kGatedSegBytes;  // bytes of one tensor's tile
-constexpr int kGatedWindow = 16;                     // records looked at together, at most
 static_assert(kGatedWorkers == kGatedSegs * 16, "16 lanes per segment");
 
 struct GatedArgs {
@@ -75,7 +86,7 @@ struct GatedArgs {
   int jobs;              // chains * blocks
   unsigned rcp_chains, rcp_groups;  // floor(2^32 / ...), for divisions
   int box;               // tokens of a TMA box
-  int look;              // records looked at together: the tiles of a chain that are worked on at a time, and some
+  int far;               // 16 records looked at together, not 8
   uint64_t wait_limit_ns;
 };
 
@@ -264,42 +275,31 @@ __device__ __forceinline__ unsigned long long rec_get(const unsigned long long* 
 // through the maps in between.  Records lie `stride` apart.  For a whole warp,
 // a lane per channel: ask() sends for the records, found() is true once every
 // lane is done.
+template <int WINDOW>
 struct GatedLook {
-  unsigned long long r[kGatedWindow];
-  __device__ __forceinline__ void ask(const unsigned long long* own, int before, int64_t stride, bool done, int look) {
+  unsigned long long r[WINDOW];
+  __device__ __forceinline__ void ask(const unsigned long long* own, int before, int64_t stride, bool done) {
 #pragma unroll
-    for (int c = 0; c < kGatedWindow; c += 2) {
-      if (c >= look) break;  // the rest is not looked at
-#pragma unroll
-      for (int i = c; i < c + 2; ++i) {
-        r[i] = ~0ull;
-        if (!done && i < before) r[i] = rec_get(own - (i + 1) * stride);
-      }
+    for (int i = 0; i < WINDOW; ++i) {
+      r[i] = ~0ull;
+      if (!done && i < before) r[i] = rec_get(own - (i + 1) * stride);
     }
   }
-  __device__ __forceinline__ bool found(bool& done, float& h, int look) {
+  __device__ __forceinline__ bool found(bool& done, float& h) {
     int at = -1;
     bool ready = !done;
 #pragma unroll
-    for (int c = 0; c < kGatedWindow; c += 2) {
-      if (c >= look) break;
-#pragma unroll
-      for (int i = c; i < c + 2; ++i) {
-        const uint32_t pb = (uint32_t)(r[i] >> 32);
-        ready = ready && pb != 0xffffffffu;
-        if (ready && at < 0 && __uint_as_float(pb) == 0.0f) at = i;
-      }
+    for (int i = 0; i < WINDOW; ++i) {
+      const uint32_t pb = (uint32_t)(r[i] >> 32);
+      ready = ready && pb != 0xffffffffu;
+      if (ready && at < 0 && __uint_as_float(pb) == 0.0f) at = i;
     }
     if (at >= 0) {
       done = true;
       h = 0.0f;
 #pragma unroll
-      for (int c = kGatedWindow - 2; c >= 0; c -= 2) {
-        if (c >= look) continue;
-#pragma unroll
-        for (int i = c + 1; i >= c; --i)
-          if (i <= at) h = fmaf(__uint_as_float((uint32_t)(r[i] >> 32)), h, __uint_as_float((uint32_t)r[i]));
-      }
+      for (int i = WINDOW - 1; i >= 0; --i)
+        if (i <= at) h = fmaf(__uint_as_float((uint32_t)(r[i] >> 32)), h, __uint_as_float((uint32_t)r[i]));
     }
     return __all_sync(0xffffffffu, done);
   }
@@ -525,7 +525,7 @@ struct GatedLoader {
 // ---------------------------------------------------------------------------
 // carrier warp: works out what enters and what leaves tiles, a lane per channel
 // ---------------------------------------------------------------------------
-template <typename TIO, bool BACKWARD>
+template <typename TIO, bool BACKWARD, int WINDOW>
 __device__ __forceinline__ void gated_carry(const GatedArgs& p, unsigned char* smem, GatedBars* bars) {
   using SM = GatedSmem<TIO, BACKWARD>;
   constexpr int kChan = SM::kChan;
@@ -550,13 +550,13 @@ __device__ __forceinline__ void gated_carry(const GatedArgs& p, unsigned char* s
       if (lane == 0) mbar_arrive(&bars->entered[par]);
     };
     // looks for what enters while the workers make the tile's map
-    GatedLook look;
+    GatedLook<WINDOW> look;
     bool done = !active || t.k == 0, mapped = false;
     bool known = __all_sync(0xffffffffu, done);
     while (!known && !mapped) {  // ends: the workers wait for nothing but loads
-      look.ask(rec, t.k, stride, done, p.look);
+      look.ask(rec, t.k, stride, done);
       mapped = __all_sync(0xffffffffu, mbar_test_wait(&bars->mapped[par], phase));
-      if (!mapped) known = look.found(done, h, p.look);
+      if (!mapped) known = look.found(done, h);
     }
     if (known) {
       tell();
@@ -570,8 +570,8 @@ __device__ __forceinline__ void gated_carry(const GatedArgs& p, unsigned char* s
     if (!known) {
       if (more) rec_put(rec, tp, th);
       uint64_t t0 = 0;
-      for (uint32_t round = 0; !look.found(done, h, p.look); ++round) {
-        look.ask(rec, t.k, stride, done, p.look);
+      for (uint32_t round = 0; !look.found(done, h); ++round) {
+        look.ask(rec, t.k, stride, done);
         if ((round & 63u) == 63u) {
           const uint64_t now = globaltimer_ns();
           if (t0 == 0) t0 = now;
@@ -643,7 +643,8 @@ __device__ __forceinline__ bool gated_begin(const GatedArgs& p, unsigned char* s
     return false;
   }
   if (threadIdx.x >= kGatedWorkers) {
-    gated_carry<TIO, BACKWARD>(p, smem, bars);
+    if (p.far) gated_carry<TIO, BACKWARD, 16>(p, smem, bars);
+    else gated_carry<TIO, BACKWARD, 8>(p, smem, bars);
     return false;
   }
 #pragma unroll

@@ -938,11 +938,11 @@ int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int 
   int sms = 0;
   if (int e = current_sms(&sms)) return e;
   const bool counted = blocks > 1 && p.chains >= 2 * sms;
-  // every record looked at costs, missing the one needed costs a round more
-  // (1 x 131072 x 2048 bf16, where about five tiles of a chain are worked on at
-  // a time: 347 us with 8 records, 384 with 16, 459 with 24; with 64 channels,
-  // one chain pair: 305, 199, 193)
-  p.look = std::min(kGatedWindow, 2 * sms / p.chains + 2);
+  // Every record looked at costs, missing the one needed costs a round more:
+  // 1 x 131072 tokens with 2048 bf16 channels (64 chains) 344 us with 8
+  // records, 384 with 16; with 512 channels 116 and 129; with 128 channels (four
+  // chains) 52 and 42; 1 x 1048576 with 64 channels 305 and 199.
+  p.far = p.chains * 32 < 2 * sms;
   // scratch: a counter and records for every pass over several tiles of time,
   // and the checkpoints that a backward call has not been given
   const bool own_ckpt = backward && !p.ckpt;
