@@ -79,6 +79,7 @@ struct GatedArgs {
   float* dh0;
   unsigned long long* rec;  // [blocks][chains][channels of a tile] records, all bits set
   int* ticket;           // tiles handed out, starting at -1; NULL: dealt by block index
+  int* gave_up;          // -1, or 0 once a wait has run out in this launch; NULL: CTAs do not wait for one another
   int64_t len, channels;
   int blocks;            // tiles along time
   int groups;            // channel groups
@@ -209,7 +210,7 @@ struct Lane4 {
 
 // ---------------------------------------------------------------------------
 // tile loads and stores.  CB: what a load moves, by the alignment of the
-// tensors and of a row of channels: 16, a TMA box of a segment; 4, cp.async of
+// tensors and of a row of channels: 16, TMA boxes of tokens; 4, cp.async of
 // 4 bytes; 2, plain loads of single elements.
 // ---------------------------------------------------------------------------
 template <int CB>
@@ -394,14 +395,18 @@ struct GatedNext {
   }
 };
 
-// Waits end: everything waited for is bounded itself.  Once an error is on
-// record nobody waits long.
+// Waits end: everything waited for is bounded itself.  Once one has run out in
+// this launch (its results are then void) nobody waits long.
 __device__ __forceinline__ uint64_t gated_limit(const GatedArgs& p) {
-  return ld_volatile(&g_device_error) == 0 ? p.wait_limit_ns : 1000000ull;
+  return p.gave_up == nullptr || ld_volatile(p.gave_up) != 0 ? p.wait_limit_ns : 1000000ull;
+}
+__device__ __forceinline__ void gated_give_up(const GatedArgs& p) {
+  record_device_error(MAMBA_ERR_TIMEOUT);
+  if (p.gave_up) atomicExch(p.gave_up, 0);
 }
 __device__ __forceinline__ void gated_wait(const GatedArgs& p, uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return;
-  if (!mbar_wait_bounded(bar, parity, 2 * gated_limit(p))) record_device_error(MAMBA_ERR_TIMEOUT);
+  if (!mbar_wait_bounded(bar, parity, 2 * gated_limit(p))) gated_give_up(p);
 }
 __device__ __forceinline__ void gated_warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -576,15 +581,16 @@ __device__ __forceinline__ void gated_carry(const GatedArgs& p, unsigned char* s
           const uint64_t now = globaltimer_ns();
           if (t0 == 0) t0 = now;
           if (__any_sync(0xffffffffu, now - t0 > gated_limit(p))) {
-            record_device_error(MAMBA_ERR_TIMEOUT);
+            gated_give_up(p);
             break;
           }
         }
       }
       tell();
     }
-    // what leaves, rounded as a reader of (P, H) rounds it
-    const float after = fmaf(tp, h, th);
+    // what leaves, as a reader of (P, H) has it: rounded so, and where P is zero
+    // without what enters, were that not a number
+    const float after = tp == 0.0f ? th : fmaf(tp, h, th);
     if (more) rec_put(rec, 0.0f, after);
     if (active) {
       if (!BACKWARD && p.ckpt) p.ckpt[((int64_t)t.b * p.blocks + t.k) * p.channels + t.c0 + lane] = h;

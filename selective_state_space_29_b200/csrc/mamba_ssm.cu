@@ -960,6 +960,7 @@ int launch_gated(GatedArgs p, int64_t batch, bool backward, unsigned flags, int 
   auto scratch_of = [&](GatedArgs q, int i) {
     if (pass > 0) {
       q.ticket = counted ? reinterpret_cast<int*>(mem + i * pass) : nullptr;
+      q.gave_up = reinterpret_cast<int*>(mem + i * pass) + 1;
       q.rec = reinterpret_cast<unsigned long long*>(mem + i * pass + 16);
     }
     return q;

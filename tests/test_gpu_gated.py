@@ -330,3 +330,43 @@ def test_no_wait_runs_out_over_many_calls(shape, dtype):
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(got, first))
     assert m.mamba_get_device_error() == m.MAMBA_OK
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_infinities_and_nan_stay_in_their_channel(dtype):
+    """Values outside the contract: other channels and earlier tokens are as
+    they would be without them, every call gives the same, and no wait runs out."""
+    d = make(2, 1100, 72, DT[dtype], "sigmoid", seed=6)
+    y0, _ = m.gated_scan(d["x"], d["gate"])
+    g0 = m.gated_scan_backward(d["x"], d["gate"], d["dy"])
+    bad = {k: v.clone() for k, v in d.items()}
+    bad["x"][0, 300, 3], bad["x"][1, 700, 40] = float("nan"), float("inf")
+    bad["gate"][0, 10, 5], bad["gate"][1, 1099, 71] = float("nan"), float("nan")
+    bad["dy"][0, 500, 7] = float("-inf")
+    y, _ = m.gated_scan(bad["x"], bad["gate"])
+    g = m.gated_scan_backward(bad["x"], bad["gate"], bad["dy"])
+    keep = torch.ones(2, 72, dtype=torch.bool, device="cuda")
+    keep[0, [3, 5, 7]] = False
+    keep[1, [40, 71]] = False
+    for a, b in ((y, y0), (g["dx"], g0["dx"]), (g["dgate"], g0["dgate"])):
+        assert torch.equal(a.transpose(1, 2)[keep], b.transpose(1, 2)[keep])
+    assert torch.equal(y[0, :300, 3], y0[0, :300, 3]) and y[0, 300:512, 3].isnan().all()
+    assert torch.equal(g["dx"][0, 501:, 7], g0["dx"][0, 501:, 7])
+    assert torch.equal(g["d_initial_state"][keep], g0["d_initial_state"][keep])
+    for _ in range(5):
+        again = m.gated_scan_backward(bad["x"], bad["gate"], bad["dy"])
+        for k in g:
+            assert torch.equal(again[k].isnan(), g[k].isnan())
+            assert torch.equal(again[k].nan_to_num(0.0, 1.0, -1.0), g[k].nan_to_num(0.0, 1.0, -1.0))
+    assert m.mamba_get_device_error() == m.MAMBA_OK
+
+
+def test_waits_are_full_length_after_an_old_error():
+    """A timeout left on record by an earlier call changes nothing."""
+    d = make(1, 5000, 64, torch.bfloat16, "log", seed=2)
+    y0, f0 = m.gated_scan(d["x"], d["gate"], gate_form="log")
+    m.mamba_debug_expire_wait(2_000_000)
+    y, f = m.gated_scan(d["x"], d["gate"], gate_form="log")
+    assert torch.equal(y, y0) and torch.equal(f, f0)
+    assert m.mamba_get_device_error(clear=True) == m.MAMBA_ERR_TIMEOUT
+    assert m.mamba_get_device_error() == m.MAMBA_OK
