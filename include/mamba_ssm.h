@@ -456,8 +456,11 @@ int mamba_mimo_supported(int64_t ranks, int64_t nstate);
  * Any number of channels; every pointer aligned to its element size.
  * Not checked: x, states and (but for minus infinity) gates finite, and
  * gates at most 0 with MAMBA_GATE_LOG.  batch * len and batch * channels
- * must stay below 2^31 (MAMBA_ERR_UNSUPPORTED).  Stream-ordered scratch, asynchrony
- * and errors as for mamba_selective_scan; an output that overlaps an input
+ * must stay below 2^31 (MAMBA_ERR_UNSUPPORTED).  A NaN or infinity stays in its
+ * channel.  Stream-ordered scratch (8 bytes per channel and block), asynchrony
+ * and errors as for mamba_selective_scan; a few long sequences take a
+ * cooperative launch, which gives MAMBA_ERR_CUDA where its blocks cannot all be
+ * on the GPU at once (two on each SM); an output that overlaps an input
  * or another output (final_state on initial_state, say) gives
  * MAMBA_ERR_INVALID_ARG, here and in the calls below.  Results do not change
  * from call to call.
