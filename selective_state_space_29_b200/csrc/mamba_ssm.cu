@@ -1044,9 +1044,12 @@ int launch_norm(NormArgs p, cudaStream_t stream) {
   using std::integral_constant;
   using T256 = integral_constant<int, 256>;
   using T1024 = integral_constant<int, 1024>;
-  // 32 elements a thread (16 where they go one by one): as few of a row, and as
-  // many rows, as CTAs of 256 threads take; few rows, one of them a thread
-  constexpr int V = E == 1 ? 16 : 32 / E, K = E == 1 ? 2 : 1;
+  // Eight 16-byte vectors a thread (16 single elements): as few of a row, and as
+  // many rows, as CTAs of 256 threads take (16384 x 2048 bf16: 28 us, with four
+  // vectors 31; 8192 x 2048 float32: 26, with sixteen 31).  Rows too few to
+  // fill the SMs so: one of them a thread (256 x 5120 bf16: 2.8 us against 3.8;
+  // 16384 x 2048 bf16 63 against 31).
+  constexpr int V = E == 1 ? 16 : 8, K = E == 1 ? 2 : 1;
   if (p.rows < (int64_t)sms * 8) {
     if (vecs <= K * 256) return run(integral_constant<int, K>{}, integral_constant<int, 1>{}, T256{});
     if (vecs <= K * 1024) return run(integral_constant<int, K>{}, integral_constant<int, 1>{}, T1024{});
