@@ -57,10 +57,11 @@ struct NormArgs {
 };
 
 __device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
-// a / n, given 1 / n rounded: one step makes up for the rounding
+// a / n, given 1 / n rounded: one step makes up for the rounding (of a sum that
+// is finite: an infinite one stays so, and its row's rstd is 0)
 __device__ __forceinline__ float over(float a, float n, float rcp) {
   const float q = a * rcp;
-  return fmaf(fmaf(-n, q, a), rcp, q);
+  return isinf(q) ? q : fmaf(fmaf(-n, q, a), rcp, q);
 }
 __device__ __forceinline__ float norm_rstd(float var) {
   float r = rsqrtf(var);  // and one Newton step

@@ -180,6 +180,38 @@ def test_helper_refusals():
     assert e.value.status == m.MAMBA_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("rows,channels", [(40, 96), (40, 1001), (3000, 512), (40, 5120)])
+def test_infinities_nan_and_squares_past_the_type(rows, channels, rms, dtype):
+    """Rows that are not finite, or whose squares are not, give what the formula
+    in 32 bits gives; the rows beside them are left alone."""
+    d = make(rows, channels, DT[dtype], seed=31)
+    y0, mean0, rstd0 = m.layer_norm(d["x"], d["weight"], d["bias"], eps=EPS, rms=rms)
+    g0 = m.layer_norm_backward(d["dy"], d["x"], d["weight"], mean0, rstd0, rms=rms)
+    x = d["x"].clone()
+    x[3, 5], x[10, channels - 1], x[17, 0] = float("inf"), float("nan"), float("-inf")
+    x[24] *= 1e25                                  # finite, its squares are not
+    odd = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    odd[[3, 10, 17, 24]] = True
+    y, mean, rstd = m.layer_norm(x, d["weight"], d["bias"], eps=EPS, rms=rms)
+    assert torch.equal(y[~odd], y0[~odd]) and torch.equal(mean[~odd], mean0[~odd]) and torch.equal(rstd[~odd], rstd0[~odd])
+    f = x[odd].float()
+    want_mean = torch.zeros(4, device="cuda") if rms else f.mean(1)
+    c = f - want_mean[:, None]
+    want_rstd = (c.square().mean(1) + EPS).rsqrt()
+    want = c * want_rstd[:, None] * d["weight"] + d["bias"]
+    assert want_rstd[3] == 0 and want[1].isnan().all()
+    assert torch.equal(mean[odd].isnan(), want_mean.isnan()) and torch.equal(mean[odd].isinf(), want_mean.isinf())
+    assert torch.equal(rstd[odd].nan_to_num(-1.0), want_rstd.nan_to_num(-1.0))   # each 0 or NaN
+    # where rstd is 0, y is the bias
+    assert torch.equal(y[odd].nan_to_num(-1e9), want.to(x.dtype).nan_to_num(-1e9))
+    g = m.layer_norm_backward(d["dy"], x, d["weight"], mean, rstd, rms=rms)
+    assert torch.equal(g["dx"][~odd], g0["dx"][~odd])
+    assert g["dx"][10].isnan().all() and (g["dx"][24] == 0).all()
+    assert torch.equal(g["dbias"], g0["dbias"])
+
+
 @pytest.mark.parametrize("rows,channels", [(3000, 256), (700, 2048), (40, 5120)])
 def test_same_bits_every_call_streams_and_graphs(rows, channels):
     d = make(rows, channels, torch.bfloat16)
