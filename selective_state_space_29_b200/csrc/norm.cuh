@@ -21,7 +21,7 @@
 // Measured (B200): forward 28 us for 16384 x 2048 bf16 (0.74 of the rate of a
 // large copy; a copy of this size takes 22), 26 us for 8192 x 2048 float32
 // (0.78); the bf16 rows are unpacked in three passes, about 15 instructions an
-// element.  Gradients 49 us for 16384 x 2048 bf16 (0.63), 41 us for 8192 x 2048
+// element.  Gradients 49 to 54 us for 16384 x 2048 bf16 (0.6), 41 us for 8192 x 2048
 // float32 (0.75): 128 registers leave 16 warps an SM, which meet once a row.
 // Vectors are 16 bytes.  SHIFT: rows that are not 16-byte aligned are covered by
 // aligned vectors that start up to E - 1 elements before them, the ones at a
